@@ -7,6 +7,9 @@ is missing or cannot be loaded, every call raises.
     W = pack(w_fp16, scales_fp16, layout=Q2_0_G128)     # ternarize + pack on the GPU
     y = gemv(W, x)                                       # x [batch][K] fp16 -> y [batch][N] fp16
     Y = gemm(W, X)                                       # X [M][K] fp16 -> Y [M][N] fp16
+    y = linear(W, x, bias, act="silu", gated=True, residual=r)   # a whole layer, one token to long prompts
+    dx, dz, db = linear_backward(W, dy, preact, act="silu", gated=True)
+    y = moe(gate_up, down, router, x, top_k=8)           # a mixture-of-experts layer for a few tokens
 """
 from __future__ import annotations
 
@@ -21,6 +24,8 @@ GROUP = 128
 GEMV_MAX_BATCH = 64
 GEMV_STATIC_WEIGHTS = 1
 DEVICE_TIMEOUT = 1
+ACTS = {"none": 0, "relu": 1, "relu2": 2, "silu": 3, "gelu": 4, "gelu_tanh": 5}
+MOE_MAX_TOKENS, MOE_MAX_EXPERTS, MOE_MAX_TOP_K, MOE_MAX_WIDTH = 64, 256, 16, 32768
 
 STATUS = {0: "TERN_OK", 1: "TERN_ERR_INVALID_ARG", 2: "TERN_ERR_UNSUPPORTED", 3: "TERN_ERR_ALIGNMENT",
           4: "TERN_ERR_WORKSPACE", 5: "TERN_ERR_INVALID_CODE", 6: "TERN_ERR_TIMEOUT", 7: "TERN_ERR_CUDA"}
@@ -53,6 +58,17 @@ class TernMatrixC(ctypes.Structure):
     _fields_ = [("layout", ctypes.c_int32), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("codes", ctypes.c_void_p), ("code_row_stride", ctypes.c_int64),
                 ("scales", ctypes.c_void_p), ("scale_row_stride", ctypes.c_int64)]
+
+
+class TernEpilogueC(ctypes.Structure):
+    _fields_ = [("act", ctypes.c_int32), ("gated", ctypes.c_int32), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("preact", ctypes.c_void_p)]
+
+
+class TernMoeLayerC(ctypes.Structure):
+    _fields_ = [("gate_up", ctypes.POINTER(TernMatrixC)), ("down", ctypes.POINTER(TernMatrixC)),
+                ("router", ctypes.c_void_p), ("experts", ctypes.c_int32), ("top_k", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("renormalize", ctypes.c_int32)]
 
 
 _lib = None
@@ -89,6 +105,15 @@ SIGNATURES = {
                                    ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p]),
     "tern_hadamard_rotate": (ctypes.c_int, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
                                             ctypes.c_void_p, ctypes.c_void_p]),
+    "tern_linear": (ctypes.c_int, [ctypes.POINTER(TernMatrixC), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                   ctypes.POINTER(TernEpilogueC), ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
+    "tern_linear_backward": (ctypes.c_int, [ctypes.POINTER(TernMatrixC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
+                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "tern_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(TernMoeLayerC), ctypes.c_int64]),
+    "tern_moe": (ctypes.c_int, [ctypes.POINTER(TernMoeLayerC), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                ctypes.c_void_p, ctypes.c_void_p]),
     "tern_device_result": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int64]),
     "tern_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tern_version": (ctypes.c_int32, []),
@@ -402,3 +427,175 @@ def gemm(W: TernMatrix, X, Y=None, status=None):
     st = lib().tern_gemm(ctypes.byref(c), _ptr(X), m, _ptr(Y), _ptr(status), _stream_handle())
     _check(st, "tern_gemm")
     return Y
+
+
+# ------------------------------------------------------------------------------- layer operators
+def _need(t, name, shape, dtype, device, contiguous=True):
+    """Checks an operand of a layer operator: a tensor of this shape and type on `device`."""
+    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name}: needs {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name}: needs a contiguous tensor")
+
+
+def _operand(t, name, shape, dtype, device):
+    """An input of a layer operator: checked, and a contiguous 16-byte aligned copy where it is neither."""
+    _need(t, name, shape, dtype, device, contiguous=False)
+    if not t.is_contiguous():
+        t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
+def _layer_matrix(W: TernMatrix, name: str, device):
+    if W.codes.device != device or W.scales.device != device:
+        raise ValueError(f"{name}: its tensors are on {W.codes.device} / {W.scales.device}, the activations on {device}")
+    return W.c()
+
+
+def _act_id(act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"act: one of {sorted(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def _on_device(device):
+    """The context in which to allocate and launch for tensors on `device`, or None when it is current."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"the layer operators run on CUDA tensors, got {device}")
+    return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+
+def linear(W: TernMatrix, x, bias=None, act: str = "none", gated: bool = False, residual=None, y=None, preact=None,
+           static_weights: bool = False, status=None):
+    """y [m][n_out] = act(x W^T + bias) (+ residual) (tern_linear), in one pass over W for few rows of x and on the
+    tcgen05 tensor cores for many; x fp16 [m][k] (or [k]: y is [n_out] then).
+
+    gated: the first half of W's rows is the gate, y = act(z[:, :n/2]) * z[:, n/2:] (+ residual), n_out = n / 2.
+    act: "none", "relu", "relu2" (squared relu), "silu", "gelu", "gelu_tanh". bias fp16 [n]; residual fp16
+    [m][n_out], may be y itself; preact: an fp16 [m][n] tensor that receives z + bias for linear_backward;
+    static_weights: no pending GPU work writes W; status: int32 tensor, DEVICE_TIMEOUT is OR-ed in when a pipeline
+    wait runs out. Raises ValueError for operands of other shapes, types or devices."""
+    device = x.device
+    other = _on_device(device)
+    if other is not None:
+        with other:
+            return linear(W, x, bias, act, gated, residual, y, preact, static_weights, status)
+    torch = _torch()
+    half = torch.float16
+    lead = x.shape[:-1]
+    if x.dim() not in (1, 2):
+        raise ValueError(f"x: needs [k] or [m][k], got {list(x.shape)}")
+    m = x.shape[0] if x.dim() == 2 else 1
+    n_out = W.n // 2 if gated else W.n
+    x = _operand(x, "x", (*lead, W.k), half, device)
+    c = _layer_matrix(W, "W", device)
+    e = TernEpilogueC(_act_id(act), 1 if gated else 0, None, None, None)
+    if bias is not None:
+        bias = _operand(bias, "bias", (W.n,), half, device)
+        e.bias = bias.data_ptr()
+    if y is None:
+        y = torch.empty((*lead, n_out), dtype=half, device=device)
+    else:
+        _need(y, "y", (*lead, n_out), half, device)
+    if residual is not None:
+        if residual is not y:
+            residual = _operand(residual, "residual", (*lead, n_out), half, device)
+        e.residual = residual.data_ptr()
+    if preact is not None:
+        _need(preact, "preact", (*lead, W.n), half, device)
+        e.preact = preact.data_ptr()
+    st = lib().tern_linear(c, x.data_ptr(), m, y.data_ptr(), e, GEMV_STATIC_WEIGHTS if static_weights else 0,
+                           status.data_ptr() if status is not None else None, torch.cuda.current_stream().cuda_stream)
+    _check(st, "tern_linear")
+    return y
+
+
+def linear_backward(W: TernMatrix, dy, preact=None, act: str = "none", gated: bool = False, need_dx: bool = True,
+                    need_dbias: bool = True, status=None):
+    """(dx fp16 [m][k], dz fp16 [m][n], dbias fp32 [n]) of linear() for dy fp16 [m][n_out] and the preact it stored
+    (tern_linear_backward); dx / dbias are None when not needed. dz is the gradient of x W^T + bias (dW = dz^T x, the
+    residual's gradient is dy); for act "none" without gating dz is dy itself and preact may be None."""
+    device = dy.device
+    other = _on_device(device)
+    if other is not None:
+        with other:
+            return linear_backward(W, dy, preact, act, gated, need_dx, need_dbias, status)
+    torch = _torch()
+    half = torch.float16
+    if dy.dim() != 2:
+        raise ValueError(f"dy: needs [m][n_out], got {list(dy.shape)}")
+    m, a = dy.shape[0], _act_id(act)
+    dy = _operand(dy, "dy", (m, W.n // 2 if gated else W.n), half, device)
+    c = _layer_matrix(W, "W", device)
+    identity = a == 0 and not gated
+    if preact is not None:
+        preact = _operand(preact, "preact", (m, W.n), half, device)
+    elif not identity:
+        raise ValueError(f"preact: needed for act {act!r} with gated={gated}")
+    dz = dy if identity else torch.empty((m, W.n), dtype=half, device=device)
+    dx = torch.empty((m, W.k), dtype=half, device=device) if need_dx else None
+    db = torch.empty((W.n,), dtype=torch.float32, device=device) if need_dbias else None
+    if not (identity and dx is None and db is None):
+        st = lib().tern_linear_backward(c, dy.data_ptr(), preact.data_ptr() if preact is not None else None, m, a,
+                                        1 if gated else 0, dx.data_ptr() if dx is not None else None,
+                                        None if identity else dz.data_ptr(), db.data_ptr() if db is not None else None,
+                                        status.data_ptr() if status is not None else None,
+                                        torch.cuda.current_stream().cuda_stream)
+        _check(st, "tern_linear_backward")
+    return dx, dz, db
+
+
+def _moe_layer(gate_up, down, router, top_k, act, renormalize, device):
+    g, d = _layer_matrix(gate_up, "gate_up", device), _layer_matrix(down, "down", device)
+    return TernMoeLayerC(ctypes.pointer(g), ctypes.pointer(d), router.data_ptr(), router.shape[0], top_k, _act_id(act),
+                         1 if renormalize else 0)
+
+
+def moe_workspace_bytes(gate_up: TernMatrix, down: TernMatrix, router, tokens: int, top_k: int) -> int:
+    """tern_moe_workspace_bytes: workspace of moe() for this many tokens (0 for arguments it refuses)."""
+    return int(lib().tern_moe_workspace_bytes(_moe_layer(gate_up, down, router, top_k, "none", False, router.device), tokens))
+
+
+def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str = "silu", renormalize: bool = True,
+        residual=None, y=None, workspace=None, return_routing: bool = False, status=None):
+    """A whole mixture-of-experts layer for up to MOE_MAX_TOKENS tokens (tern_moe): x fp16 [tokens][d] is routed by
+    softmax(x router^T), router fp16 [experts][d], to the top_k most probable experts (ties to the lower index), and
+    y = sum over them of p * down_e(act(gate_e x) * up_e x) (+ residual).
+
+    gate_up: packed [experts * 2f][d], for each expert f gate rows and then f up rows; down: packed [experts * d][f].
+    workspace: a uint8 tensor of moe_workspace_bytes() (any contents; allocated when None). With return_routing
+    returns (y, weights fp32 [tokens][top_k], ids int32 [tokens][top_k])."""
+    device = x.device
+    other = _on_device(device)
+    if other is not None:
+        with other:
+            return moe(gate_up, down, router, x, top_k, act, renormalize, residual, y, workspace, return_routing, status)
+    torch = _torch()
+    half = torch.float16
+    if x.dim() != 2 or router.dim() != 2:
+        raise ValueError(f"x and router: need [tokens][d] and [experts][d], got {list(x.shape)} and {list(router.shape)}")
+    tokens, d = x.shape[0], gate_up.k
+    x = _operand(x, "x", (tokens, d), half, device)
+    router = _operand(router, "router", (router.shape[0], d), half, device)
+    layer = _moe_layer(gate_up, down, router, top_k, act, renormalize, device)
+    if y is None:
+        y = torch.empty((tokens, d), dtype=half, device=device)
+    else:
+        _need(y, "y", (tokens, d), half, device)
+    if residual is not None and residual is not y:
+        residual = _operand(residual, "residual", (tokens, d), half, device)
+    if workspace is None:
+        workspace = torch.empty(max(1, int(lib().tern_moe_workspace_bytes(layer, tokens))), dtype=torch.uint8, device=device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs a contiguous tensor on {device}")
+    weights = ids = None
+    if return_routing:
+        weights = torch.empty((tokens, max(0, top_k)), dtype=torch.float32, device=device)
+        ids = torch.empty((tokens, max(0, top_k)), dtype=torch.int32, device=device)
+    st = lib().tern_moe(layer, x.data_ptr(), tokens, residual.data_ptr() if residual is not None else None, y.data_ptr(),
+                        weights.data_ptr() if return_routing else None, ids.data_ptr() if return_routing else None,
+                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                        status.data_ptr() if status is not None else None, torch.cuda.current_stream().cuda_stream)
+    _check(st, "tern_moe")
+    return (y, weights, ids) if return_routing else y

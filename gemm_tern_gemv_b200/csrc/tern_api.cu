@@ -6,7 +6,7 @@
 #include <vector>
 
 #include "tern_fwht.cuh"
-#include "tern_internal.cuh"
+#include "tern_layer.cuh"
 
 namespace tern {
 
@@ -301,6 +301,104 @@ tern_status tern_hadamard_rotate(const uint16_t* x, int64_t batch, int64_t k, co
   if (batch > (int64_t)INT32_MAX / (k / 1024) || batch * k > (int64_t)1 << 40) return TERN_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 1u) return TERN_ERR_ALIGNMENT;
   return from_cuda(launch_rotate(x, batch, k, signs, y, static_cast<cudaStream_t>(stream)));
+}
+
+// Checks of the epilogue shared by the linear layer and its backward.
+static tern_status check_act(int32_t act, int32_t gated, int64_t n) {
+  if (act < TERN_ACT_NONE || act > TERN_ACT_GELU_TANH) return TERN_ERR_UNSUPPORTED;
+  if (gated != 0 && gated != 1) return TERN_ERR_INVALID_ARG;
+  if (gated && n % 2) return TERN_ERR_INVALID_ARG;
+  return TERN_OK;
+}
+static inline bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
+
+tern_status tern_linear(const tern_matrix* W, const uint16_t* x, int64_t m, uint16_t* y, const tern_epilogue* epilogue,
+                        uint32_t flags, uint32_t* device_status, void* stream) {
+  if (flags & ~(uint32_t)TERN_GEMV_STATIC_WEIGHTS) return TERN_ERR_INVALID_ARG;
+  tern_status s = check_matrix(W);
+  if (s != TERN_OK) return s;
+  const tern_epilogue none{};
+  const tern_epilogue& ep = epilogue ? *epilogue : none;
+  s = check_act(ep.act, ep.gated, W->n);
+  if (s != TERN_OK) return s;
+  if (m < 1 || m > (int64_t)INT32_MAX || !x || !y) return TERN_ERR_INVALID_ARG;
+  if (!aligned16(x)) return TERN_ERR_ALIGNMENT;
+  if (!aligned2(y) || !aligned2(ep.bias) || !aligned2(ep.residual) || !aligned2(ep.preact)) return TERN_ERR_ALIGNMENT;
+  if (device_status && (reinterpret_cast<uintptr_t>(device_status) & 3u)) return TERN_ERR_ALIGNMENT;
+  const Epilogue e{ep.act, ep.gated, ep.bias, ep.residual, ep.preact};
+  return from_cuda(launch_linear(*W, x, m, y, e, flags, device_status, static_cast<cudaStream_t>(stream)));
+}
+
+tern_status tern_linear_backward(const tern_matrix* W, const uint16_t* dy, const uint16_t* preact, int64_t m, int32_t act,
+                                 int32_t gated, uint16_t* dx, uint16_t* dz, float* dbias, uint32_t* device_status,
+                                 void* stream) {
+  tern_status s = check_matrix(W);
+  if (s != TERN_OK) return s;
+  s = check_act(act, gated, W->n);
+  if (s != TERN_OK) return s;
+  if (m < 1 || m > (int64_t)INT32_MAX || !dy || (!dx && !dz && !dbias)) return TERN_ERR_INVALID_ARG;
+  const bool identity = act == TERN_ACT_NONE && !gated;
+  if (!identity && !preact) return TERN_ERR_INVALID_ARG;
+  if (!identity && dx && !dz) return TERN_ERR_INVALID_ARG;
+  if (!aligned16(dz) || (identity && !dz ? !aligned16(dy) : !aligned2(dy)) || !aligned2(preact) || !aligned2(dx))
+    return TERN_ERR_ALIGNMENT;
+  if (reinterpret_cast<uintptr_t>(dbias) & 3u) return TERN_ERR_ALIGNMENT;
+  if (device_status && (reinterpret_cast<uintptr_t>(device_status) & 3u)) return TERN_ERR_ALIGNMENT;
+  return from_cuda(launch_linear_backward(*W, dy, preact, m, act, gated, dx, dz, dbias, device_status,
+                                          static_cast<cudaStream_t>(stream)));
+}
+
+static tern_status check_moe(const tern_moe_layer* L, int64_t tokens) {
+  if (!L) return TERN_ERR_INVALID_ARG;
+  tern_status s = check_matrix(L->gate_up);
+  if (s != TERN_OK) return s;
+  s = check_matrix(L->down);
+  if (s != TERN_OK) return s;
+  if (L->act < TERN_ACT_NONE || L->act > TERN_ACT_GELU_TANH) return TERN_ERR_UNSUPPORTED;
+  if (L->renormalize != 0 && L->renormalize != 1) return TERN_ERR_INVALID_ARG;
+  if (L->experts < 1 || L->top_k < 1 || L->top_k > L->experts || tokens < 1) return TERN_ERR_INVALID_ARG;
+  const int64_t d = L->gate_up->k, f = L->down->k;
+  if (L->gate_up->n != 2 * f * L->experts || L->down->n != d * L->experts) return TERN_ERR_INVALID_ARG;
+  if (L->experts > TERN_MOE_MAX_EXPERTS || L->top_k > TERN_MOE_MAX_TOP_K || tokens > TERN_MOE_MAX_TOKENS ||
+      d > TERN_MOE_MAX_WIDTH || f > TERN_MOE_MAX_WIDTH)
+    return TERN_ERR_UNSUPPORTED;
+  return TERN_OK;
+}
+
+size_t tern_moe_workspace_bytes(const tern_moe_layer* layer, int64_t tokens) {
+  if (check_moe(layer, tokens) != TERN_OK) return 0;
+  return moe_plan(tokens, layer->gate_up->k, layer->down->k, layer->experts, layer->top_k).bytes;
+}
+
+tern_status tern_moe(const tern_moe_layer* layer, const uint16_t* x, int64_t tokens, const uint16_t* residual, uint16_t* y,
+                     float* weights, int32_t* ids, void* workspace, size_t workspace_bytes, uint32_t* device_status,
+                     void* stream) {
+  const tern_status s = check_moe(layer, tokens);
+  if (s != TERN_OK) return s;
+  if (!x || !y || !layer->router) return TERN_ERR_INVALID_ARG;
+  if (!aligned16(x) || !aligned16(layer->router)) return TERN_ERR_ALIGNMENT;
+  if (!aligned2(y) || !aligned2(residual) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
+      (reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
+    return TERN_ERR_ALIGNMENT;
+  const MoePlan plan = moe_plan(tokens, layer->gate_up->k, layer->down->k, layer->experts, layer->top_k);
+  if (!workspace || workspace_bytes < plan.bytes) return TERN_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return TERN_ERR_ALIGNMENT;
+  MoeParams p{};
+  p.x = x;
+  p.router = layer->router;
+  p.residual = residual;
+  p.y = y;
+  p.weights = weights;
+  p.ids = ids;
+  p.tokens = (int)tokens;
+  p.d = (int)layer->gate_up->k;
+  p.f = (int)layer->down->k;
+  p.experts = layer->experts;
+  p.top_k = layer->top_k;
+  p.act = layer->act;
+  p.renormalize = layer->renormalize;
+  p.status = device_status;
+  return from_cuda(launch_moe(*layer->gate_up, *layer->down, p, plan, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 tern_status tern_device_result(uint32_t device_status, int64_t invalid_count) {

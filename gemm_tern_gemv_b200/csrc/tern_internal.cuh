@@ -109,4 +109,31 @@ cudaError_t launch_gemv_t(const tern_matrix& W, const uint16_t* dy, int batch, u
 cudaError_t launch_rotate(const uint16_t* x, int64_t batch, int64_t k, const int8_t* signs, uint16_t* y,
                           cudaStream_t st);
 
+// ---- layer operators ------------------------------------------------------------------------
+struct Epilogue;  // tern_layer.cuh
+cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, uint16_t* y, const Epilogue& e,
+                          uint32_t flags, uint32_t* status, cudaStream_t st);
+// dz may be null when it equals dy (no activation, not gated), dx and db when they are not wanted
+cudaError_t launch_linear_backward(const tern_matrix& W, const uint16_t* dy, const uint16_t* z, int64_t m, int act,
+                                   int gated, uint16_t* dx, uint16_t* dz, float* db, uint32_t* status, cudaStream_t st);
+
+constexpr int kMoeMaxExperts = TERN_MOE_MAX_EXPERTS;
+struct MoeParams {
+  const uint16_t* x;         // [tokens][d]
+  const uint16_t* router;    // [experts][d]
+  const uint16_t* residual;  // [tokens][d] or null
+  uint16_t* y;               // [tokens][d]
+  float* weights;            // [tokens][top_k]
+  int32_t* ids;              // [tokens][top_k]
+  float* h;                  // [tokens * top_k][f] expert activations
+  uint32_t* status;          // device status word or null
+  int tokens, d, f, experts, top_k, act, renormalize;
+};
+struct MoePlan {  // workspace offsets
+  size_t ids, weights, h, bytes;
+};
+MoePlan moe_plan(int64_t tokens, int64_t d, int64_t f, int experts, int top_k);
+cudaError_t launch_moe(const tern_matrix& G, const tern_matrix& D, MoeParams p, const MoePlan& plan, void* workspace,
+                       cudaStream_t st);
+
 }  // namespace tern

@@ -1,0 +1,72 @@
+// Shared by the layer operators (fused linear layer, its backward, mixture of experts): activations
+// and their derivatives in fp32, the epilogue's arguments, and the decode of a single weight.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "tern_internal.cuh"
+
+namespace tern {
+
+// What follows z = W x of a linear layer: y = act(z + bias) (+ residual), or with `gated` (n = 2f)
+// y = act(z[0:f]) * z[f:2f] (+ residual). Everything in fp32, one rounding to fp16 at the end.
+struct Epilogue {
+  int act;                   // tern_act
+  int gated;
+  const uint16_t* bias;      // [n] or null
+  const uint16_t* residual;  // [m][n_out] or null
+  uint16_t* preact;          // [m][n] or null: z + bias, rounded to fp16
+};
+
+__device__ __forceinline__ float h2f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
+__device__ __forceinline__ uint16_t f2h(float f) { return __half_as_ushort(__float2half_rn(f)); }
+
+// gelu is z Phi(z) with Phi(z) = erfc(-z / sqrt 2) / 2 (no cancellation for negative z); its tanh form
+// is z sigmoid(u), u = sqrt(8 / pi) (z + 0.044715 z^3), since (1 + tanh(u / 2)) / 2 = sigmoid(u).
+__device__ __forceinline__ float gelu_tanh_u(float z) { return 1.5957691216057308f * (z + 0.044715f * z * z * z); }
+
+__device__ __forceinline__ float act_fwd(int act, float z) {
+  switch (act) {
+    case TERN_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
+    case TERN_ACT_RELU2: return z < 0.f ? 0.f : z * z;
+    case TERN_ACT_SILU: return z / (1.f + expf(-z));
+    case TERN_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case TERN_ACT_GELU_TANH: return z / (1.f + expf(-gelu_tanh_u(z)));
+    default: return z;
+  }
+}
+
+// act'(z). The sigmoid's complement is taken as 1 / (1 + e^u), not 1 - sigmoid(u), so that the tails
+// keep their relative precision.
+__device__ __forceinline__ float act_bwd(int act, float z) {
+  switch (act) {
+    case TERN_ACT_RELU: return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // 0 at 0; NaN stays NaN
+    case TERN_ACT_RELU2: return z > 0.f ? 2.f * z : (z <= 0.f ? 0.f : z);
+    case TERN_ACT_SILU: {
+      const float s = 1.f / (1.f + expf(-z)), c = 1.f / (1.f + expf(z));
+      return s + z * s * c;
+    }
+    case TERN_ACT_GELU: return 0.5f * erfcf(-0.70710678118654752f * z) + 0.39894228040143268f * z * expf(-0.5f * z * z);
+    case TERN_ACT_GELU_TANH: {
+      const float u = gelu_tanh_u(z), s = 1.f / (1.f + expf(-u)), c = 1.f / (1.f + expf(u));
+      return s + z * s * c * 1.5957691216057308f * (1.f + 0.134145f * z * z);
+    }
+    default: return 1.f;
+  }
+}
+
+// t of weight k of a packed row (any layout); an invalid code gives an unspecified t.
+__device__ __forceinline__ float decode_t(int layout, const uint8_t* row, int64_t k) {
+  if (layout == TERN_Q2_0_G128) {
+    const int f = (row[k >> 2] >> (2 * (int)(k & 3))) & 3;
+    return (float)((f & 1) - (f & 2));
+  }
+  if (layout == TERN_Q1_0_G128) return ((row[k >> 3] >> (int)(k & 7)) & 1) ? 1.f : -1.f;
+  int v = row[k / 5];
+  for (int i = (int)(k % 5); i > 0; i--) v /= 3;
+  return (float)(v % 3) - 1.f;
+}
+
+}  // namespace tern

@@ -315,6 +315,103 @@ TERN_API size_t tern_gemv_t_workspace_bytes(const tern_matrix* W, int64_t batch)
 TERN_API tern_status tern_gemv_t(const tern_matrix* W, const uint16_t* dy, int64_t batch, uint16_t* dx,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- layer operators ------------------------------------------------------------------------- */
+/* The layer around the product: what a decoder step or a straight-through-estimator training step
+ * does right before and after W x, in the same kernels. These entry points are engineering additions;
+ * the pages describe the products (eq. w_i = s_g t_i and the fused unpack, above) and the models built
+ * from them (attention projections, gated feed-forward blocks), not these kernels. */
+
+typedef enum tern_act {
+  TERN_ACT_NONE = 0,
+  TERN_ACT_RELU = 1,       /* max(z, 0) */
+  TERN_ACT_RELU2 = 2,      /* max(z, 0)^2 */
+  TERN_ACT_SILU = 3,       /* z / (1 + e^-z) */
+  TERN_ACT_GELU = 4,       /* z Phi(z), Phi the normal distribution function */
+  TERN_ACT_GELU_TANH = 5   /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+} tern_act;
+
+/* What tern_linear does with z = W x. Zero-initialise and set what you need. */
+typedef struct tern_epilogue {
+  int32_t act;               /* tern_act */
+  int32_t gated;             /* 0, or 1: rows [0, n/2) of W are the gate, rows [n/2, n) the up projection (n even) */
+  const uint16_t* bias;      /* device fp16 [n] or NULL, added to z */
+  const uint16_t* residual;  /* device fp16 [m][n_out] or NULL, added to the result; may be y itself */
+  uint16_t* preact;          /* device fp16 [m][n] or NULL: z + bias, rounded, for tern_linear_backward */
+} tern_epilogue;
+
+/* One linear layer, y = act(z + bias) + residual with z = W x, or with `gated`
+ * y = act(z[0 .. n/2)) * z[n/2 .. n) + residual (both halves with their bias). n_out = n, or n / 2 gated.
+ * z, the bias, the activation and the residual are taken in fp32 and y is rounded once (preact is a
+ * rounded copy of z + bias; y does not depend on whether it is asked for). Any m >= 1, any n.
+ *   x   device fp16 [m][k], contiguous, 16-byte aligned;  y  device fp16 [m][n_out], contiguous
+ *   y, preact must not overlap x or one another; residual may be y (same element, in place)
+ *   flags          0 or TERN_GEMV_STATIC_WEIGHTS: nothing pending on the GPU writes W, so a call with few
+ *                  rows of x may read its first weights while the preceding kernel of the stream ends
+ *   device_status  device uint32 or NULL, as for tern_gemm
+ * Infinities and NaN in x reach y as the formula has them (0 * inf = NaN). The result depends only on
+ * the arguments and the device (fixed summation order). No workspace.
+ * Errors: TERN_ERR_INVALID_ARG (also n odd with gated, unknown flags), TERN_ERR_UNSUPPORTED (layout or
+ * act), TERN_ERR_ALIGNMENT, TERN_ERR_CUDA. */
+TERN_API tern_status tern_linear(const tern_matrix* W, const uint16_t* x, int64_t m, uint16_t* y,
+                                 const tern_epilogue* epilogue, uint32_t flags, uint32_t* device_status,
+                                 void* stream);
+
+/* The gradients of tern_linear with respect to z, bias and x (the straight-through step treats W = s t
+ * as the weights, see tern_gemv_t; dW = dz^T x has no packed operand and stays with the caller; the
+ * residual's gradient is dy):
+ *   dz = dy * act'(z), gated: dz[0 .. n/2) = dy * z_up * act'(z_gate), dz[n/2 .. n) = dy * act(z_gate);
+ *   dbias[j] = sum over rows of dz[.][j] (fp32, from unrounded dz, fixed order);  dx = dz W with the
+ *   rounded dz (fp32 accumulation, one rounding).
+ * act'(0) = 0 for relu.
+ *   dy      device fp16 [m][n_out];  preact  device fp16 [m][n], what tern_linear stored (may be NULL
+ *           for TERN_ACT_NONE without gating)
+ *   dx      device fp16 [m][k] or NULL;  dbias  device fp32 [n] or NULL
+ *   dz      device fp16 [m][n], 16-byte aligned; may be NULL for TERN_ACT_NONE without gating (dz is dy
+ *           then, which must be 16-byte aligned), or when dx is NULL
+ *   outputs must not overlap the inputs or one another. Any m >= 1, any n. No workspace.
+ * Errors: TERN_ERR_INVALID_ARG (also: all outputs NULL), TERN_ERR_UNSUPPORTED, TERN_ERR_ALIGNMENT,
+ * TERN_ERR_CUDA. */
+TERN_API tern_status tern_linear_backward(const tern_matrix* W, const uint16_t* dy, const uint16_t* preact, int64_t m,
+                                          int32_t act, int32_t gated, uint16_t* dx, uint16_t* dz, float* dbias,
+                                          uint32_t* device_status, void* stream);
+
+#define TERN_MOE_MAX_TOKENS 64
+#define TERN_MOE_MAX_EXPERTS 256
+#define TERN_MOE_MAX_TOP_K 16
+#define TERN_MOE_MAX_WIDTH 32768  /* largest d and f */
+
+/* A mixture-of-experts layer: experts of gate [f][d], up [f][d] and down [d][f] matrices. */
+typedef struct tern_moe_layer {
+  const tern_matrix* gate_up;  /* [experts * 2f][d]: for each expert f gate rows, then f up rows */
+  const tern_matrix* down;     /* [experts * d][f] */
+  const uint16_t* router;      /* device fp16 [experts][d], contiguous, 16-byte aligned */
+  int32_t experts;             /* 1 .. TERN_MOE_MAX_EXPERTS */
+  int32_t top_k;               /* 1 .. min(experts, TERN_MOE_MAX_TOP_K) experts per token */
+  int32_t act;                 /* tern_act on the gate */
+  int32_t renormalize;         /* 1: the chosen probabilities are divided by their sum */
+} tern_moe_layer;
+
+/* Bytes of device workspace tern_moe needs; 0 on invalid arguments. Host only. */
+TERN_API size_t tern_moe_workspace_bytes(const tern_moe_layer* layer, int64_t tokens);
+
+/* The whole layer for 1 .. TERN_MOE_MAX_TOKENS tokens:
+ *   p = softmax(router x[t]); ids[t] = the top_k most probable experts, most probable first, ties to
+ *   the lower index; weights[t][j] = p[ids[t][j]] (divided by their sum with renormalize);
+ *   y[t] = sum_j weights[t][j] * down_e (act(gate_e x[t]) * (up_e x[t])) + residual[t],  e = ids[t][j].
+ * Logits and their order in fp64, everything else in fp32, y rounded once. Experts without a token are
+ * not read. A token whose logits hold a NaN gets valid ids and NaN weights.
+ *   x  device fp16 [tokens][d], 16-byte aligned;  y  device fp16 [tokens][d]
+ *   residual   device fp16 [tokens][d] or NULL; may be y or x
+ *   weights    device fp32 [tokens][top_k] or NULL;  ids  device int32 [tokens][top_k] or NULL
+ *   workspace  device, >= tern_moe_workspace_bytes, 16-byte aligned, contents do not matter. Calls that
+ *              share a workspace must not overlap on the GPU.
+ *   device_status  device uint32 or NULL, as for tern_gemm
+ * Errors: TERN_ERR_INVALID_ARG (also matrices whose shapes do not fit together), TERN_ERR_UNSUPPORTED
+ * (layout, act, or a size over the limits above), TERN_ERR_ALIGNMENT, TERN_ERR_WORKSPACE, TERN_ERR_CUDA. */
+TERN_API tern_status tern_moe(const tern_moe_layer* layer, const uint16_t* x, int64_t tokens, const uint16_t* residual,
+                              uint16_t* y, float* weights, int32_t* ids, void* workspace, size_t workspace_bytes,
+                              uint32_t* device_status, void* stream);
+
 /* ---- activation-side block Hadamard rotation ------------------------------------------------ */
 
 /* y = R x for every 1024-element block of every row, R = H S / 32 ("Ternary Bonsai 2 27B ..."
