@@ -35,6 +35,27 @@ int sm_count() {
   return cache[dev];
 }
 
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  constexpr int kSlots = 128, kDevices = 64;  // kernels of the library that ask, devices that are remembered
+  static std::mutex mu;
+  static const void* known[kSlots];
+  static uint64_t done[kSlots];  // bit: device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(mu);
+  int i = 0;
+  while (i < kSlots && known[i] && known[i] != kernel) i++;
+  const bool keep = i < kSlots && dev < kDevices;
+  if (keep && known[i] == kernel && (done[i] >> dev & 1)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && keep) {
+    known[i] = kernel;
+    done[i] |= 1ull << dev;
+  }
+  return e;
+}
+
 }  // namespace tern
 
 using namespace tern;

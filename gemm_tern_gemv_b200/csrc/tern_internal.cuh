@@ -21,6 +21,10 @@ int64_t row_bytes(int32_t layout, int64_t k);
 // Number of streaming multiprocessors of the current device (cached per device).
 int sm_count();
 
+// Lets `kernel` use up to `bytes` of dynamic shared memory on the current device (asked of the driver once
+// per kernel and device).
+cudaError_t allow_smem(const void* kernel, size_t bytes);
+
 // 2-D TMA tensor map over [outer][inner] elements with rows row_stride_bytes apart, boxes of
 // box_outer x box_inner, out-of-range elements read as zero; encoded once per distinct argument set.
 bool tmap_2d(CUtensorMap* out, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,

@@ -1,10 +1,32 @@
 // Fused linear layer y = act(W x + b) (+ residual), gated or not, on packed ternary weights.
-#include "tern_layer.cuh"
+//
+// Few rows of x (up to kFewRows): linear_rows_kernel, the register core of tern_rows.cuh. One CTA per SM
+// owns a run of 16-row tiles (gated: 8 gate rows and their 8 up rows, so that both halves of an output meet
+// in one thread); its warps cut K, their partial sums meet in shared memory in warp order, and the epilogue
+// runs on the fp32 sums.
+// More rows: see linear_kernel.
+#include "tern_rows.cuh"
 
 namespace tern {
 namespace {
 
 constexpr int kTok = 4;  // rows of x per warp
+
+__device__ __forceinline__ void epilogue(const Epilogue& e, int64_t n, int64_t nout, int64_t t, int64_t o, float z0, float z1,
+                                         uint16_t* y) {
+  if (e.bias) {
+    z0 += h2f(e.bias[o]);
+    if (e.gated) z1 += h2f(e.bias[o + nout]);
+  }
+  if (e.preact) {
+    e.preact[t * n + o] = f2h(z0);
+    if (e.gated) e.preact[t * n + o + nout] = f2h(z1);
+  }
+  float v = act_fwd(e.act, z0);
+  if (e.gated) v *= z1;
+  if (e.residual) v += h2f(e.residual[t * nout + o]);
+  y[t * nout + o] = f2h(v);
+}
 
 // One warp per output feature (and its gate partner): lanes stride over K, fp32 accumulation.
 __global__ void __launch_bounds__(128) linear_kernel(tern_matrix W, const uint16_t* __restrict__ x, int64_t m,
@@ -33,29 +55,97 @@ __global__ void __launch_bounds__(128) linear_kernel(tern_matrix W, const uint16
       for (int i = 1; i < kTok; i++)
         if (lane == i) z[h] = acc[h][i];
     }
-    const int64_t t = m0 + lane;
-    if (e.bias) {
-      z[0] += h2f(e.bias[o]);
-      if (e.gated) z[1] += h2f(e.bias[o + nout]);
-    }
-    if (e.preact) {
-      e.preact[t * W.n + o] = f2h(z[0]);
-      if (e.gated) e.preact[t * W.n + o + nout] = f2h(z[1]);
-    }
-    float v = act_fwd(e.act, z[0]);
-    if (e.gated) v *= z[1];
-    if (e.residual) v += h2f(e.residual[t * nout + o]);
-    y[t * nout + o] = f2h(v);
+    epilogue(e, W.n, nout, m0 + lane, o, z[0], z[1], y);
   }
 }
+
+struct RowsParams {
+  rows::Mat mat;
+  rows::Map map;
+  rows::Split split;
+  const uint16_t* x;
+  uint16_t* y;
+  Epilogue e;
+  int64_t n, nout;
+  int tiles, tokens, early;
+};
+
+template <int L, int MODE, int NT>
+__global__ void __launch_bounds__(rows::kThreads, 1) linear_rows_kernel(const __grid_constant__ RowsParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  sm100::griddep_launch_dependents();
+  if (!p.early) sm100::griddep_wait();
+  const int t0 = (int)((int64_t)blockIdx.x * p.tiles / gridDim.x), t1 = (int)((int64_t)(blockIdx.x + 1) * p.tiles / gridDim.x);
+  const rows::HalfRows xs{p.x, p.mat.K, nullptr};
+  rows::Product<L, MODE, NT> prod;
+  prod.run(smem, p.split, p.mat, p.map, t0, t1, xs, p.tokens, [&] { if (p.early) sm100::griddep_wait(); },
+           [&](int tile, int r, int t, float z0, float z1) {
+             epilogue(p.e, p.n, p.nout, t, (int64_t)tile * p.map.step + r, z0, z1, p.y);
+           });
+}
+
+constexpr size_t kRoom = 227 * 1024;  // shared memory of a CTA
+
+template <int L, int MODE, int NT>
+cudaError_t launch_rows(RowsParams& p, cudaStream_t st) {
+  using P = rows::Product<L, MODE, NT>;
+  const int grid = std::min(p.tiles, sm_count());
+  if (!rows::plan_split<P>((p.tiles + grid - 1) / grid, p.mat.units, kRoom, &p.split)) return cudaErrorInvalidValue;
+  const size_t smem = P::smem_bytes(p.split);
+  const void* kern = reinterpret_cast<const void*>(&linear_rows_kernel<L, MODE, NT>);
+  const cudaError_t err = allow_smem(kern, kRoom);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(rows::kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, linear_rows_kernel<L, MODE, NT>, p);
+}
+
+// m <= 2: the int8 form; otherwise fp16 column tiles of 8 rows of x (4 with two slots per unit).
+template <int L>
+cudaError_t pick_rows(RowsParams& p, cudaStream_t st) {
+  if (p.tokens <= rows::Geo<L, rows::kInt8>::kTok) return launch_rows<L, rows::kInt8, 1>(p, st);
+  if (p.tokens <= 2) return launch_rows<L, rows::kInt8, 2>(p, st);
+  const int nt = (p.tokens + rows::Geo<L, rows::kFp16>::kTok - 1) / rows::Geo<L, rows::kFp16>::kTok;
+  if (nt == 1) return launch_rows<L, rows::kFp16, 1>(p, st);
+  if (nt == 2) return launch_rows<L, rows::kFp16, 2>(p, st);
+  return launch_rows<L, rows::kFp16, 4>(p, st);
+}
+
+constexpr int kFewRows = 16;
 
 }  // namespace
 
 cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, uint16_t* y, const Epilogue& e,
                           uint32_t flags, uint32_t* status, cudaStream_t st) {
-  (void)flags;
   (void)status;
   const int64_t nout = e.gated ? W.n / 2 : W.n;
+  if (m <= kFewRows) {
+    RowsParams p{};
+    p.mat = rows::Mat{static_cast<const uint8_t*>(W.codes), W.scales, W.code_row_stride, W.scale_row_stride, (int)W.k,
+                      (int)row_bytes(W.layout, W.k), (int)(W.k / kGroup), (int)((row_bytes(W.layout, W.k) + 31) / 32)};
+    p.map = e.gated ? rows::Map{0, nout, (int)nout, 8, 0} : rows::Map{0, 0, (int)nout, 16, 8};
+    p.x = x;
+    p.y = y;
+    p.e = e;
+    p.n = W.n;
+    p.nout = nout;
+    p.tiles = (int)((nout + p.map.step - 1) / p.map.step);
+    p.tokens = (int)m;
+    p.early = (flags & TERN_GEMV_STATIC_WEIGHTS) ? 1 : 0;
+    switch (W.layout) {
+      case TERN_Q2_0_G128: return pick_rows<TERN_Q2_0_G128>(p, st);
+      case TERN_T3_5PB_G128: return pick_rows<TERN_T3_5PB_G128>(p, st);
+      default: return pick_rows<TERN_Q1_0_G128>(p, st);
+    }
+  }
   const dim3 grid((unsigned)((nout + 3) / 4), (unsigned)std::min<int64_t>((m + kTok - 1) / kTok, 65535));
   linear_kernel<<<grid, 128, 0, st>>>(W, x, m, y, e);
   return cudaGetLastError();
