@@ -109,7 +109,7 @@ SIGNATURES = {
                                    ctypes.POINTER(TernEpilogueC), ctypes.c_uint32, ctypes.c_void_p, ctypes.c_void_p]),
     "tern_linear_backward": (ctypes.c_int, [ctypes.POINTER(TernMatrixC), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
                                             ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
-                                            ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+                                            ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
     "tern_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(TernMoeLayerC), ctypes.c_int64]),
     "tern_moe": (ctypes.c_int, [ctypes.POINTER(TernMoeLayerC), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                 ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
@@ -515,7 +515,8 @@ def linear_backward(W: TernMatrix, dy, preact=None, act: str = "none", gated: bo
                     need_dbias: bool = True, status=None):
     """(dx fp16 [m][k], dz fp16 [m][n], dbias fp32 [n]) of linear() for dy fp16 [m][n_out] and the preact it stored
     (tern_linear_backward); dx / dbias are None when not needed. dz is the gradient of x W^T + bias (dW = dz^T x, the
-    residual's gradient is dy); for act "none" without gating dz is dy itself and preact may be None."""
+    residual's gradient is dy), its rows padded to 16 bytes where n is not a multiple of 8; for act "none" without gating
+    it equals dy (may be dy itself) and preact may be None."""
     device = dy.device
     other = _on_device(device)
     if other is not None:
@@ -533,16 +534,21 @@ def linear_backward(W: TernMatrix, dy, preact=None, act: str = "none", gated: bo
         preact = _operand(preact, "preact", (m, W.n), half, device)
     elif not identity:
         raise ValueError(f"preact: needed for act {act!r} with gated={gated}")
-    dz = dy if identity else torch.empty((m, W.n), dtype=half, device=device)
     dx = torch.empty((m, W.k), dtype=half, device=device) if need_dx else None
     db = torch.empty((W.n,), dtype=torch.float32, device=device) if need_dbias else None
-    if not (identity and dx is None and db is None):
-        st = lib().tern_linear_backward(c, dy.data_ptr(), preact.data_ptr() if preact is not None else None, m, a,
-                                        1 if gated else 0, dx.data_ptr() if dx is not None else None,
-                                        None if identity else dz.data_ptr(), db.data_ptr() if db is not None else None,
-                                        status.data_ptr() if status is not None else None,
-                                        torch.cuda.current_stream().cuda_stream)
-        _check(st, "tern_linear_backward")
+    if identity and not need_dx and not need_dbias:
+        return None, dy, None
+    # rows of dz are 16-byte aligned: padded (and for act "none" a copy of dy) where n is not a multiple of 8
+    own_dz = not identity or (need_dx and W.n % 8 != 0)
+    dz = torch.empty((m, (W.n + 7) // 8 * 8), dtype=half, device=device) if own_dz else dy
+    st = lib().tern_linear_backward(c, dy.data_ptr(), preact.data_ptr() if preact is not None else None, m, a,
+                                    1 if gated else 0, dx.data_ptr() if need_dx else None, dz.data_ptr() if own_dz else None,
+                                    dz.stride(0), db.data_ptr() if need_dbias else None,
+                                    status.data_ptr() if status is not None else None,
+                                    torch.cuda.current_stream().cuda_stream)
+    _check(st, "tern_linear_backward")
+    if own_dz and dz.shape[1] != W.n:
+        dz = dz[:, :W.n]
     return dx, dz, db
 
 

@@ -351,8 +351,8 @@ tern_status tern_linear(const tern_matrix* W, const uint16_t* x, int64_t m, uint
 }
 
 tern_status tern_linear_backward(const tern_matrix* W, const uint16_t* dy, const uint16_t* preact, int64_t m, int32_t act,
-                                 int32_t gated, uint16_t* dx, uint16_t* dz, float* dbias, uint32_t* device_status,
-                                 void* stream) {
+                                 int32_t gated, uint16_t* dx, uint16_t* dz, int64_t dz_row_stride, float* dbias,
+                                 uint32_t* device_status, void* stream) {
   tern_status s = check_matrix(W);
   if (s != TERN_OK) return s;
   s = check_act(act, gated, W->n);
@@ -360,12 +360,14 @@ tern_status tern_linear_backward(const tern_matrix* W, const uint16_t* dy, const
   if (m < 1 || m > (int64_t)INT32_MAX || !dy || (!dx && !dz && !dbias)) return TERN_ERR_INVALID_ARG;
   const bool identity = act == TERN_ACT_NONE && !gated;
   if (!identity && !preact) return TERN_ERR_INVALID_ARG;
-  if (!identity && dx && !dz) return TERN_ERR_INVALID_ARG;
-  if (!aligned16(dz) || (identity && !dz ? !aligned16(dy) : !aligned2(dy)) || !aligned2(preact) || !aligned2(dx))
+  if (dx && !dz && (!identity || W->n % 8)) return TERN_ERR_INVALID_ARG;
+  if (dz && dz_row_stride < W->n) return TERN_ERR_INVALID_ARG;
+  if (dz && dz_row_stride % 8) return TERN_ERR_ALIGNMENT;
+  if (!aligned16(dz) || (dx && !dz ? !aligned16(dy) : !aligned2(dy)) || !aligned2(preact) || !aligned2(dx))
     return TERN_ERR_ALIGNMENT;
   if (reinterpret_cast<uintptr_t>(dbias) & 3u) return TERN_ERR_ALIGNMENT;
   if (device_status && (reinterpret_cast<uintptr_t>(device_status) & 3u)) return TERN_ERR_ALIGNMENT;
-  return from_cuda(launch_linear_backward(*W, dy, preact, m, act, gated, dx, dz, dbias, device_status,
+  return from_cuda(launch_linear_backward(*W, dy, preact, m, act, gated, dx, dz, dz_row_stride, dbias, device_status,
                                           static_cast<cudaStream_t>(stream)));
 }
 

@@ -29,6 +29,9 @@ cudaError_t allow_smem(const void* kernel, size_t bytes);
 // box_outer x box_inner, out-of-range elements read as zero; encoded once per distinct argument set.
 bool tmap_2d(CUtensorMap* out, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
              uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
+// The same, encoded anew (well under a microsecond) and remembered nowhere.
+bool tmap_2d_new(CUtensorMap* out, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                 uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw);
 
 // ---- launchers (arguments already validated by the C ABI layer) ----------------------------
 // prev / flips: optional previous packing of the same matrix and the flip counter it feeds
@@ -119,7 +122,14 @@ cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, ui
                           uint32_t flags, uint32_t* status, cudaStream_t st);
 // dz may be null when it equals dy (no activation, not gated), dx and db when they are not wanted
 cudaError_t launch_linear_backward(const tern_matrix& W, const uint16_t* dy, const uint16_t* z, int64_t m, int act,
-                                   int gated, uint16_t* dx, uint16_t* dz, float* db, uint32_t* status, cudaStream_t st);
+                                   int gated, uint16_t* dx, uint16_t* dz, int64_t dz_stride, float* db, uint32_t* status,
+                                   cudaStream_t st);
+// The many-row products: z = x W^T with the epilogue, and dx = dz W (dz rows dz_stride halves apart, a
+// multiple of 8). Any m, any n.
+cudaError_t launch_layer_gemm(const tern_matrix& W, const uint16_t* x, int64_t m, uint16_t* y, const Epilogue& e,
+                              uint32_t* status, cudaStream_t st);
+cudaError_t launch_layer_gemm_t(const tern_matrix& W, const uint16_t* dz, int64_t dz_stride, int64_t m, uint16_t* dx,
+                                uint32_t* status, cudaStream_t st);
 
 constexpr int kMoeMaxExperts = TERN_MOE_MAX_EXPERTS;
 struct MoeParams {

@@ -31,9 +31,9 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
     case TERN_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case TERN_ACT_RELU2: return z < 0.f ? 0.f : z * z;
-    case TERN_ACT_SILU: return z / (1.f + expf(-z));
+    case TERN_ACT_SILU:
+    case TERN_ACT_GELU_TANH: return __fdividef(z, 1.f + __expf(act == TERN_ACT_SILU ? -z : -gelu_tanh_u(z)));
     case TERN_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
-    case TERN_ACT_GELU_TANH: return z / (1.f + expf(-gelu_tanh_u(z)));
     default: return z;
   }
 }
@@ -54,6 +54,20 @@ __device__ __forceinline__ float act_bwd(int act, float z) {
       return s + z * s * c * 1.5957691216057308f * (1.f + 0.134145f * z * z);
     }
     default: return 1.f;
+  }
+}
+
+// act(z) and act'(z) together.
+__device__ __forceinline__ void act_both(int act, float z, float* f, float* df) {
+  if (act == TERN_ACT_SILU || act == TERN_ACT_GELU_TANH) {
+    const float u = act == TERN_ACT_SILU ? z : gelu_tanh_u(z);
+    const float s = 1.f / (1.f + expf(-u)), c = 1.f / (1.f + expf(u));
+    const float du = act == TERN_ACT_SILU ? 1.f : 1.5957691216057308f * (1.f + 0.134145f * z * z);
+    *f = z * s;
+    *df = s + z * s * c * du;
+  } else {
+    *f = act_fwd(act, z);
+    *df = act_bwd(act, z);
   }
 }
 

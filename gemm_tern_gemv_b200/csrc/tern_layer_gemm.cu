@@ -1,0 +1,584 @@
+// Many-row products of the layer operators on tcgen05 tensor cores, weights decoded into tensor memory:
+//     forward     z[t][n]  = sum_k x[t][k]  s[n][k/128] t[n][k]     (tern_linear)
+//     transposed  dx[t][k] = sum_n dz[t][n] s[n][k/128] t[n][k]     (tern_linear_backward)
+//
+// A CTA computes tiles of 128 weight rows (forward) or weight columns (transposed) by `bn` rows of x, 64
+// terms of the sum at a time. In D = A B^T the decoded weights are A (M = 128), the activations B.
+//   * What bounds it. Per 64 terms the MMAs take bn / 256 x 512 cycles; B is written to shared memory by
+//     TMA and read by the MMAs, together 128 bytes a cycle at the MMAs' full rate, which is all that
+//     shared memory gives. So A must not go through it too: it lives in tensor memory. Decoder warps turn
+//     codes into fp16 s t in registers (exact) and store them with tcgen05.st; 32 columns hold 64 terms.
+//   * Tensor memory: two accumulators of up to 192 columns, so that the epilogue of a tile runs beside the
+//     MMAs of the next, and a ring of four A stages (4 x 32 columns).
+//   * Warps: 0 TMA, 1 MMA, 4-7 epilogue, 8-15 decode (two sets of four; a set takes every other 64 terms).
+//   * bn is chosen by the host so that the tiles fill whole waves of CTAs.
+//   * Transposed: A's rows are the columns of the packed rows, whose group is one scale per packed row.
+//     ldmatrix.trans hands a lane 16-bit pieces of two adjacent rows; each field of theirs is a finished
+//     pair of A, and the 16x128b store shape has rows by lane / 4 and columns by lane % 4 as ldmatrix has.
+//   * Base-3 bytes go through a table of five 2-bit fields each and become words of Q2's form first.
+// Every wait is bounded in wall time; on expiry the CTA raises its abort flag, ORs TERN_DEVICE_TIMEOUT into
+// the caller's status word, lets copies and MMAs in flight end, frees tensor memory and exits.
+#include <cuda.h>
+
+#include "sm100.cuh"
+#include "tern_layer.cuh"
+
+namespace tern {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128;      // rows of A per tile
+constexpr int BK = 64;       // terms per stage (one 128-byte swizzle row of fp16)
+constexpr int kMaxBN = 192;  // rows of x per tile
+constexpr int STAGES = 6;    // TMA ring
+constexpr int ASTAGES = 4;   // A ring in tensor memory
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512, kACol = 2 * kMaxBN;  // accumulators at 0 and kMaxBN, A from kACol
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+constexpr int X_BYTES = kMaxBN * BK * 2;
+constexpr int P_BYTES = BM * 32;  // codes of a stage: forward 128 rows x 16 or 32 bytes, transposed 64 x 16, 32 or 48
+constexpr int OFF_P = STAGES * X_BYTES;
+constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;  // transposed base-3: the two sets' tiles in Q2's form [64][32]
+constexpr int OFF_S = OFF_Q + 2 * 64 * 32;       // transposed: the two sets' 64 scales
+constexpr int OFF_LUT = OFF_S + 2 * 64 * 2;
+constexpr int OFF_BAR = OFF_LUT + 256 * 4;
+constexpr int NUM_BARS = 2 * STAGES + 2 * ASTAGES + 4 + 1;
+constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
+constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + slack to align the base to 1024
+
+struct Params {
+  int64_t m;             // rows of x
+  int64_t n;             // packed rows
+  int64_t k;             // weights of a packed row
+  int64_t nout;          // outputs of a row: n, n / 2 (gated) or k (transposed)
+  int terms;             // length of the sum: k or n
+  int bn, rtiles, mtiles;
+  const uint16_t* scales;
+  int64_t sstride;
+  uint16_t* y;
+  Epilogue e;
+  uint32_t* status;
+};
+
+// ---- tensor memory stores and A operands from it -----------------------------------------------------
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+      "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+      "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+// 16 rows x 32 columns: r[2i] is (row lane / 4, column 4 i + lane % 4), r[2i + 1] the same 8 rows below.
+__device__ __forceinline__ void tmem_st_16x128b_x8(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+
+// ---- decoding ------------------------------------------------------------------------------------------
+// fp16 pair s t from the pair's fp16 values 2 t: halved first, so that no scale can overflow.
+__device__ __forceinline__ uint32_t scaled(uint32_t two_t, __half2 s2) {
+  const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&two_t), __half2half2(__ushort_as_half(0x3800))), s2);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Codes 2j and 2j + 1 of a word (16 two's-complement fields): one multiply brings them to bits 14..15 and
+// 30..31, where a field is the sign and top exponent bit of +-2.0 (or 0).
+__device__ __forceinline__ uint32_t pair_q2(uint32_t w, int j) {
+  const int jj = j & 3, a = 14 - 4 * jj;
+  const uint32_t x = (j < 4 ? w : w >> 16) & (0xFu << (4 * jj));
+  return (x * ((1u << a) + (1u << (a + 14)))) & 0xC000C000u;
+}
+// Sign bits p and p + 1 (p even, <= 14): +-1.0 (0x3C00 / 0xBC00).
+__device__ __forceinline__ uint32_t pair_q1(uint32_t w, int p) {
+  const uint32_t x = w & (3u << p);
+  return ((x * ((1u << (15 - p)) + (1u << (30 - p)))) & 0x80008000u) ^ 0xBC00BC00u;
+}
+// 64 trits from digit R0 of p[0] on, as four words of 16 two's-complement fields.
+template <int R0>
+__device__ __forceinline__ void t3_words_r(const uint8_t* p, const uint32_t* lut, uint32_t (&w)[4]) {
+  constexpr int NB = (R0 + 63) / 5 + 1;
+  w[0] = w[1] = w[2] = w[3] = 0;
+#pragma unroll
+  for (int j = 0; j < NB; j++) {
+    const uint32_t f = lut[p[j]];
+    const int at = 10 * j - 2 * R0;  // bit of the byte's first field
+    if (at < 0) {
+      w[0] |= f >> -at;
+    } else {
+      w[at >> 5] |= f << (at & 31);
+      if ((at & 31) > 22 && (at >> 5) < 3) w[(at >> 5) + 1] |= f >> (32 - (at & 31));
+    }
+  }
+}
+__device__ __forceinline__ void t3_words(int r0, const uint8_t* p, const uint32_t* lut, uint32_t (&w)[4]) {
+  switch (r0) {
+    case 0: t3_words_r<0>(p, lut, w); break;
+    case 1: t3_words_r<1>(p, lut, w); break;
+    case 2: t3_words_r<2>(p, lut, w); break;
+    case 3: t3_words_r<3>(p, lut, w); break;
+    default: t3_words_r<4>(p, lut, w); break;
+  }
+}
+
+// ---- the kernel ------------------------------------------------------------------------------------------
+template <int LAYOUT, bool TRANS>
+__global__ void __launch_bounds__(kThreads, 1)
+layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // TMA -> decoders, MMA
+  uint64_t* empty = full + STAGES;                               // MMA -> TMA
+  uint64_t* dfull = empty + STAGES;                              // decoders -> MMA
+  uint64_t* dempty = dfull + ASTAGES;                            // MMA -> decoders
+  uint64_t* tfull = dempty + ASTAGES;                            // MMA -> epilogue (2)
+  uint64_t* tempty = tfull + 2;                                  // epilogue -> MMA (2)
+  uint64_t* drain = tempty + 2;                                  // MMA completion on abort
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
+  uint32_t* lut = reinterpret_cast<uint32_t*>(smem + OFF_LUT);
+
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int tiles = p.rtiles * p.mtiles;
+  const int kblocks = (p.terms + BK - 1) / BK;
+  const bool gated = !TRANS && p.e.gated;
+  const int step = gated ? 64 : BM;  // outputs of a tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < STAGES; i++) { mbar_init(full + i, 1); mbar_init(empty + i, 1); }
+    for (int i = 0; i < ASTAGES; i++) { mbar_init(dfull + i, 4); mbar_init(dempty + i, 1); }
+    for (int i = 0; i < 2; i++) { mbar_init(tfull + i, 1); mbar_init(tempty + i, 4); }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) { prefetch_tmap(&tmap_x); prefetch_tmap(&tmap_w); }
+  if (LAYOUT == TERN_T3_5PB_G128) {
+    for (int v = threadIdx.x; v < 256; v += kThreads) {
+      uint32_t f = 0, r = (uint32_t)v;
+      if (v < 243) {
+#pragma unroll
+        for (int d = 0; d < 5; d++) { f |= ((r % 3u + 3u) & 3u) << (2 * d); r /= 3u; }  // c - 1 as two bits
+      }
+      lut[v] = f;  // an invalid byte reads as five t = 0
+    }
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------------ TMA producer
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      constexpr int P_ROW = TRANS ? (LAYOUT == TERN_Q1_0_G128 ? 16 : LAYOUT == TERN_Q2_0_G128 ? 32 : 48)
+                                  : (LAYOUT == TERN_T3_5PB_G128 ? 32 : 16);
+      const uint32_t bytes = (uint32_t)p.bn * BK * 2 + (TRANS ? BK : BM) * P_ROW;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+        const int r0 = (tile / p.mtiles) * step, m0 = (tile % p.mtiles) * p.bn;
+        for (int kb = 0; kb < kblocks; kb++, it++) {
+          const int s = it % STAGES;
+          if (!mbar_wait_bounded(empty + s, ((it / STAGES) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full + s, bytes);
+          tma_load_2d(smem + s * X_BYTES, &tmap_x, full + s, kb * BK, m0);
+          uint8_t* dst = smem + OFF_P + s * P_BYTES;
+          if (TRANS) {  // columns r0 .. r0 + 127 of rows kb * 64 ..
+            const int px = LAYOUT == TERN_Q2_0_G128 ? r0 / 4 : LAYOUT == TERN_Q1_0_G128 ? r0 / 8 : (r0 / 5) & ~15;
+            tma_load_2d(dst, &tmap_w, full + s, px, kb * BK);
+          } else {
+            const int px = LAYOUT == TERN_Q2_0_G128 ? kb * (BK / 4) : LAYOUT == TERN_Q1_0_G128 ? (kb * (BK / 8)) & ~15 : ((kb * BK) / 5) & ~15;
+            tma_load_2d(dst, &tmap_w, full + s, px, r0);
+            if (gated) tma_load_2d(dst + 64 * P_ROW, &tmap_w, full + s, px, (int)p.nout + r0);
+          }
+        }
+      }
+      // copies in flight must land before the CTA's shared memory goes away (the last round's are waited
+      // for by the decoders unless they gave up)
+      if (!ok) {
+        const uint64_t t0 = globaltimer_ns();
+        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; i++)
+          while (!mbar_try_wait(full + i % STAGES, (i / STAGES) & 1u) && globaltimer_ns() - t0 < kWaitNs / 4) {
+          }
+      }
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      const uint32_t idesc = idesc_f16_f32(BM, p.bn);
+      uint32_t it = 0, lt = 0;
+      bool ok = true, issued = false;
+      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, lt++) {
+        const uint32_t acc = lt & 1u;
+        if (!mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t tmem_d = tmem + acc * kMaxBN;
+        for (int kb = 0; kb < kblocks; kb++, it++) {
+          const int s = it % STAGES, d = it % ASTAGES;
+          if (!mbar_wait_bounded(full + s, (it / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs) ||
+              !mbar_wait_bounded(dfull + d, (it / ASTAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t bdesc = smem_desc_sw128(smem_u32(smem + s * X_BYTES));
+          const uint32_t a = tmem + kACol + d * 32;
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; kk++) mma_f16_ts(tmem_d, a + 8 * kk, bdesc + 2 * kk, idesc, (kb | kk) != 0);
+          issued = true;
+          mma_commit(empty + s);
+          mma_commit(dempty + d);
+        }
+        if (!ok) break;
+        mma_commit(tfull + acc);
+      }
+      if (!ok && issued) {  // the MMAs already issued must end before tensor memory is freed
+        mma_commit(drain);
+        const uint64_t t0 = globaltimer_ns();
+        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs / 4) {
+        }
+      }
+    }
+  } else if (warp >= 4 && warp < 8) {
+    // ------------------------------------------------------------------ epilogue
+    const int quad = warp & 3;
+    // the A row of this lane is output `o` of the tile (of the gate, or with `up` of the up projection)
+    int o;
+    const bool up = gated && lane >= 16;
+    if (!TRANS) o = gated ? quad * 16 + (lane & 15) : quad * 32 + lane;
+    else if (LAYOUT == TERN_Q1_0_G128) o = 16 * (lane & 7) + 4 * quad + (lane >> 3);
+    else o = 64 * (quad >> 1) + 8 * (lane & 7) + 4 * (quad & 1) + (lane >> 3);
+    uint32_t lt = 0;
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, lt++) {
+      const int64_t j = (int64_t)(tile / p.mtiles) * step + o;  // output column
+      const int64_t m0 = (int64_t)(tile % p.mtiles) * p.bn;
+      const bool in = j < p.nout;
+      const float bias = !TRANS && p.e.bias && in ? h2f(p.e.bias[j + (up ? p.nout : 0)]) : 0.f;
+      const uint32_t acc = lt & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs))) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + acc * kMaxBN + ((uint32_t)(quad * 32) << 16);
+      const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);  // rows of x in this tile
+#pragma unroll 1
+      for (int c0 = 0; c0 < cols; c0 += 16) {
+        uint32_t r[16];
+        tmem_ld_32x32b_x16(taddr + c0, r);
+        uint16_t* y = p.y + (m0 + c0) * p.nout + j;
+        const uint16_t* res = !TRANS && p.e.residual ? p.e.residual + (m0 + c0) * p.nout + j : nullptr;
+        uint16_t rv[16];
+        if (!TRANS && res && !gated) {
+#pragma unroll
+          for (int i = 0; i < 16; i++) rv[i] = in && c0 + i < cols ? res[i * p.nout] : (uint16_t)0;
+        }
+        tmem_ld_wait();
+        if (TRANS || !gated) {
+#pragma unroll
+          for (int i = 0; i < 16; i++) {
+            if (!in || c0 + i >= cols) continue;
+            float v = __uint_as_float(r[i]);
+            if (!TRANS) {
+              v += bias;
+              if (p.e.preact) p.e.preact[(m0 + c0 + i) * p.n + j] = f2h(v);
+              v = act_fwd(p.e.act, v);
+              if (res) v += h2f(rv[i]);
+            }
+            y[i * p.nout] = f2h(v);
+          }
+        } else {
+          // lanes l and l + 16 hold the gate and the up sum of one output; of two rows of x the lower lane
+          // finishes the first, the upper one the second
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float z0 = __uint_as_float(r[i]) + bias, z1 = __uint_as_float(r[i + 1]) + bias;
+            const float got = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
+            const int t = i + (up ? 1 : 0);
+            if (p.e.preact && in) {
+              uint16_t* z = p.e.preact + (m0 + c0 + i) * p.n + j + (up ? p.nout : 0);
+              if (c0 + i < cols) z[0] = f2h(z0);
+              if (c0 + i + 1 < cols) z[p.n] = f2h(z1);
+            }
+            if (!in || c0 + t >= cols) continue;
+            float v = act_fwd(p.e.act, up ? got : z0) * (up ? z1 : got);
+            if (res) v += h2f(res[t * p.nout]);
+            y[t * p.nout] = f2h(v);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(tempty + acc);
+    }
+  } else if (warp >= 8) {
+    // ------------------------------------------------------------------ decoders
+    const int quad = warp & 3, set = (warp - 8) >> 2, st = threadIdx.x & 127;
+    const uint32_t a_lane = tmem + kACol + ((uint32_t)(quad * 32) << 16);
+    uint32_t it = 0;
+    bool ok = true;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
+      const int r0 = (tile / p.mtiles) * step;
+      // forward: this lane's row of A is packed row `row`, at row `src` of the stage's codes
+      const int src = gated ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
+      const int64_t row = gated ? (int64_t)r0 + (src & 63) + (src >= 64 ? p.nout : 0) : (int64_t)r0 + src;
+      const uint16_t* srow = p.scales + (row < p.n ? row : p.n - 1) * p.sstride;
+      const int first = (int)((it ^ (uint32_t)set) & 1u);  // the set's first block of this tile
+      // transposed: thread st < 64 of the set brings the scale of one packed row; forward: the lane's own
+      auto fetch = [&](int kb) -> uint16_t {
+        if (kb >= kblocks) return 0;
+        if (!TRANS) return __ldg(srow + (kb * BK) / kGroup);
+        const int64_t n = (int64_t)kb * BK + st;
+        return st < 64 && n < p.n ? __ldg(p.scales + n * p.sstride + r0 / kGroup) : (uint16_t)0;
+      };
+      uint16_t sc = fetch(first);
+      for (int kb = first; kb < kblocks; kb += 2) {
+        const uint32_t i = it + kb;
+        const int s = i % STAGES, d = i % ASTAGES;
+        const uint16_t cur = sc;
+        sc = fetch(kb + 2);
+        bool fine = mbar_wait_bounded(full + s, (i / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        fine = fine && mbar_wait_bounded(dempty + d, ((i / ASTAGES) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        const uint8_t* P = smem + OFF_P + s * P_BYTES;
+        if constexpr (!TRANS) {
+          if (!__all_sync(0xffffffffu, fine)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const __half2 s2 = __half2half2(__ushort_as_half(cur));
+          uint32_t o[32];
+          if (LAYOUT == TERN_Q1_0_G128) {
+            const uint2 w = *reinterpret_cast<const uint2*>(P + src * 16 + 8 * (kb & 1));
+#pragma unroll
+            for (int j = 0; j < 32; j++) {
+              const uint32_t one = pair_q1((j < 16 ? w.x : w.y) >> (j & 8 ? 16 : 0), 2 * (j & 7));
+              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&one), s2);
+              o[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+          } else {
+            uint32_t w[4];
+            if (LAYOUT == TERN_Q2_0_G128) {
+              const uint4 u = *reinterpret_cast<const uint4*>(P + src * 16);
+              w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+            } else {
+              const int t0 = kb * BK;
+              t3_words(t0 % 5, P + src * 32 + ((t0 / 5) & 15), lut, w);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; j++) o[j] = scaled(pair_q2(w[j >> 3], j & 7), s2);
+          }
+          tmem_st_32x32b_x32(a_lane + d * 32, o);
+        } else {
+          // scales (and base-3 words) of the block are shared by the set's four warps, which all leave together
+          uint16_t* S = reinterpret_cast<uint16_t*>(smem + OFF_S) + set * 64;
+          uint8_t* Q = smem + OFF_Q + set * 64 * 32;
+          bar_sync(1 + set, 128);  // the set is done with the block before
+          if (st < 64) S[st] = cur;
+          if (!fine) *abort_flag = 1;
+          if (LAYOUT == TERN_T3_5PB_G128 && fine) {
+            const int t0 = r0 + 64 * (st & 1);
+            uint32_t w[4];
+            t3_words(t0 % 5, P + (st >> 1) * 48 + t0 / 5 - ((r0 / 5) & ~15), lut, w);
+            *reinterpret_cast<uint4*>(Q + (st >> 1) * 32 + 16 * (st & 1)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          bar_sync(1 + set, 128);
+          if (*abort_flag) fine = false;
+          // the verdict is the same in all four warps: the flag is raised before the barrier above or by
+          // others at any time, so it is agreed on once more
+          fine = __all_sync(0xffffffffu, fine);
+          int all = fine ? 1 : 0;
+          asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+                       : "+r"(all) : "r"(1 + set) : "memory");
+          if (!all) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          // columns of 16 bits of the codes: Q2 eight fields (two column groups of 16 bytes), binary 16 bits
+          const int group = LAYOUT == TERN_Q1_0_G128 ? 0 : quad >> 1;
+          const uint32_t base = LAYOUT == TERN_T3_5PB_G128 ? smem_u32(Q) : smem_u32(P);
+          constexpr int pitch = LAYOUT == TERN_Q1_0_G128 ? 16 : 32;
+          uint32_t R[8], sp[8];
+#pragma unroll
+          for (int h = 0; h < 2; h++) {
+            uint32_t v[4];
+            ldmatrix_x4_trans(base + (uint32_t)((32 * h + lane) * pitch + 16 * group), v);
+#pragma unroll
+            for (int q = 0; q < 4; q++) R[4 * h + q] = v[q];
+          }
+#pragma unroll
+          for (int q = 0; q < 8; q++) sp[q] = *reinterpret_cast<const uint32_t*>(S + 8 * q + 2 * (lane & 3));
+          const int f0 = LAYOUT == TERN_Q1_0_G128 ? 4 * quad : 4 * (quad & 1);  // the warp's first field
+          const uint32_t up_mul = LAYOUT == TERN_Q1_0_G128 ? 1u << (12 - f0) : 1u << (8 - 2 * f0);
+#pragma unroll
+          for (int half = 0; half < 2; half++) {
+            uint32_t o[16];
+#pragma unroll
+            for (int q = 0; q < 8; q++) {
+#pragma unroll
+              for (int b = 0; b < 2; b++) {
+                const int f = 2 * half + b;  // field f0 + f of both halves of R[q]
+                const __half2 s2 = *reinterpret_cast<const __half2*>(&sp[q]);
+                if (LAYOUT == TERN_Q1_0_G128) {
+                  const uint32_t x = R[q] & (0x00010001u << f0 << f);  // bit f0 + f -> bit 15
+                  const uint32_t one = (x * (up_mul << (3 - f))) ^ 0xBC00BC00u;
+                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&one), s2);
+                  o[2 * q + b] = *reinterpret_cast<const uint32_t*>(&v);
+                } else {
+                  const uint32_t x = R[q] & (0x00030003u << (2 * f0) << (2 * f));  // field -> bits 14..15
+                  o[2 * q + b] = scaled(x * (up_mul << (6 - 2 * f)), s2);
+                }
+              }
+            }
+            tmem_st_16x128b_x8(a_lane + ((uint32_t)(16 * half) << 16) + d * 32, o);
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(dfull + d);
+      }
+      it += kblocks;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int LAYOUT, bool TRANS>
+cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, Params& p, cudaStream_t st) {
+  CUtensorMap mx, mw;
+  if (!tmap_2d_new(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)p.terms, (uint64_t)p.m, (uint64_t)xstride * 2, BK,
+                   (uint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  // codes as bytes [n][row data]: reads past them give zero
+  const uint64_t data = LAYOUT == TERN_Q2_0_G128 ? W.k / 4 : LAYOUT == TERN_Q1_0_G128 ? W.k / 8 : (W.k + 4) / 5;
+  const uint32_t width = TRANS ? (LAYOUT == TERN_Q1_0_G128 ? 16 : LAYOUT == TERN_Q2_0_G128 ? 32 : 48)
+                               : (LAYOUT == TERN_T3_5PB_G128 ? 32 : 16);
+  if (!tmap_2d_new(&mw, CU_TENSOR_MAP_DATA_TYPE_UINT8, W.codes, data, (uint64_t)W.n, (uint64_t)W.code_row_stride, width,
+                   TRANS || p.e.gated ? 64 : BM, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
+  const void* kern = reinterpret_cast<const void*>(&layer_gemm_kernel<LAYOUT, TRANS>);
+  const cudaError_t e = allow_smem(kern, SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (int64_t)p.rtiles * p.mtiles;
+  layer_gemm_kernel<LAYOUT, TRANS><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, SMEM_BYTES, st>>>(mx, mw, p);
+  return cudaGetLastError();
+}
+
+// Rows of x per tile: the multiple of 16 up to kMaxBN that makes the waves of tiles cheapest. A tile costs
+// its columns plus what does not shrink with them (the decoding of A, about 64 columns' worth of MMAs).
+int pick_bn(int64_t m, int64_t rtiles, int sms) {
+  int best = kMaxBN;
+  double cost = -1;
+  for (int bn = 16; bn <= kMaxBN; bn += 16) {
+    if (bn > 16 && bn - 16 >= m) break;
+    const int64_t tiles = rtiles * ((m + bn - 1) / bn), waves = (tiles + sms - 1) / sms;
+    const double c = (double)waves * std::max(bn, 96);
+    if (cost < 0 || c <= cost) {
+      cost = c;
+      best = bn;
+    }
+  }
+  return best;
+}
+
+template <bool TRANS>
+cudaError_t dispatch(const tern_matrix& W, const uint16_t* x, int64_t xstride, Params& p, cudaStream_t st) {
+  switch (W.layout) {
+    case TERN_Q2_0_G128: return launch_t<TERN_Q2_0_G128, TRANS>(W, x, xstride, p, st);
+    case TERN_T3_5PB_G128: return launch_t<TERN_T3_5PB_G128, TRANS>(W, x, xstride, p, st);
+    default: return launch_t<TERN_Q1_0_G128, TRANS>(W, x, xstride, p, st);
+  }
+}
+
+Params common(const tern_matrix& W, int64_t m, uint32_t* status) {
+  Params p{};
+  p.m = m;
+  p.n = W.n;
+  p.k = W.k;
+  p.scales = W.scales;
+  p.sstride = W.scale_row_stride;
+  p.status = status;
+  return p;
+}
+
+}  // namespace
+
+cudaError_t launch_layer_gemm(const tern_matrix& W, const uint16_t* x, int64_t m, uint16_t* y, const Epilogue& e,
+                              uint32_t* status, cudaStream_t st) {
+  Params p = common(W, m, status);
+  p.nout = e.gated ? W.n / 2 : W.n;
+  p.terms = (int)W.k;
+  p.y = y;
+  p.e = e;
+  const int step = e.gated ? 64 : BM;
+  p.rtiles = (int)((p.nout + step - 1) / step);
+  p.bn = pick_bn(m, p.rtiles, sm_count());
+  const int64_t mt = (m + p.bn - 1) / p.bn;
+  if (mt * p.rtiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+  p.mtiles = (int)mt;
+  return dispatch<false>(W, x, W.k, p, st);
+}
+
+cudaError_t launch_layer_gemm_t(const tern_matrix& W, const uint16_t* dz, int64_t dz_stride, int64_t m, uint16_t* dx,
+                                uint32_t* status, cudaStream_t st) {
+  Params p = common(W, m, status);
+  p.nout = W.k;
+  p.terms = (int)W.n;
+  p.y = dx;
+  p.rtiles = (int)(W.k / BM);
+  p.bn = pick_bn(m, p.rtiles, sm_count());
+  const int64_t mt = (m + p.bn - 1) / p.bn;
+  if (mt * p.rtiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+  p.mtiles = (int)mt;
+  return dispatch<true>(W, dz, dz_stride, p, st);
+}
+
+}  // namespace tern

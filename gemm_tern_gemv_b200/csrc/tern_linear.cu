@@ -4,13 +4,11 @@
 // owns a run of 16-row tiles (gated: 8 gate rows and their 8 up rows, so that both halves of an output meet
 // in one thread); its warps cut K, their partial sums meet in shared memory in warp order, and the epilogue
 // runs on the fp32 sums.
-// More rows: see linear_kernel.
+// More rows: the tensor-core kernel of tern_layer_gemm.cu.
 #include "tern_rows.cuh"
 
 namespace tern {
 namespace {
-
-constexpr int kTok = 4;  // rows of x per warp
 
 __device__ __forceinline__ void epilogue(const Epilogue& e, int64_t n, int64_t nout, int64_t t, int64_t o, float z0, float z1,
                                          uint16_t* y) {
@@ -26,37 +24,6 @@ __device__ __forceinline__ void epilogue(const Epilogue& e, int64_t n, int64_t n
   if (e.gated) v *= z1;
   if (e.residual) v += h2f(e.residual[t * nout + o]);
   y[t * nout + o] = f2h(v);
-}
-
-// One warp per output feature (and its gate partner): lanes stride over K, fp32 accumulation.
-__global__ void __launch_bounds__(128) linear_kernel(tern_matrix W, const uint16_t* __restrict__ x, int64_t m,
-                                                     uint16_t* y, Epilogue e) {
-  const int lane = threadIdx.x & 31;
-  const int64_t nout = e.gated ? W.n / 2 : W.n;
-  const int64_t o = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-  if (o >= nout) return;
-  const uint8_t* codes = static_cast<const uint8_t*>(W.codes);
-  for (int64_t m0 = (int64_t)blockIdx.y * kTok; m0 < m; m0 += (int64_t)gridDim.y * kTok) {
-    const int nt = (int)(m - m0 < kTok ? m - m0 : kTok);
-    float acc[2][kTok] = {};
-    for (int h = 0; h < (e.gated ? 2 : 1); h++) {
-      const int64_t n = o + h * nout;
-      for (int64_t k = lane; k < W.k; k += 32) {
-        const float w = decode_t(W.layout, codes + n * W.code_row_stride, k) * h2f(W.scales[n * W.scale_row_stride + k / kGroup]);
-        for (int i = 0; i < nt; i++) acc[h][i] = fmaf(w, h2f(x[(m0 + i) * W.k + k]), acc[h][i]);
-      }
-      for (int i = 0; i < kTok; i++)
-        for (int s = 16; s; s >>= 1) acc[h][i] += __shfl_xor_sync(0xffffffffu, acc[h][i], s);
-    }
-    if (lane >= nt) continue;
-    float z[2];
-    for (int h = 0; h < 2; h++) {
-      z[h] = acc[h][0];
-      for (int i = 1; i < kTok; i++)
-        if (lane == i) z[h] = acc[h][i];
-    }
-    epilogue(e, W.n, nout, m0 + lane, o, z[0], z[1], y);
-  }
 }
 
 struct RowsParams {
@@ -125,7 +92,6 @@ constexpr int kFewRows = 16;
 
 cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, uint16_t* y, const Epilogue& e,
                           uint32_t flags, uint32_t* status, cudaStream_t st) {
-  (void)status;
   const int64_t nout = e.gated ? W.n / 2 : W.n;
   if (m <= kFewRows) {
     RowsParams p{};
@@ -146,9 +112,7 @@ cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, ui
       default: return pick_rows<TERN_Q1_0_G128>(p, st);
     }
   }
-  const dim3 grid((unsigned)((nout + 3) / 4), (unsigned)std::min<int64_t>((m + kTok - 1) / kTok, 65535));
-  linear_kernel<<<grid, 128, 0, st>>>(W, x, m, y, e);
-  return cudaGetLastError();
+  return launch_layer_gemm(W, x, m, y, e, status, st);
 }
 
 }  // namespace tern

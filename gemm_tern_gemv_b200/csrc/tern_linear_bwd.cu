@@ -1,66 +1,152 @@
-// Backward of the fused linear layer: dz = dy * act'(z), db = sum over rows of dz, dx = dz W.
+// Backward of the fused linear layer: dz = dy * act'(z), dbias = sum over rows of dz, dx = dz W.
+//
+// dz and dbias come from one pass (dz_kernel), bound by HBM: dy and z are read once, dz is written once.
+// A CTA takes 32 x VEC columns and a slice of the rows, a warp every eighth of them, a lane VEC columns
+// (16 bytes where rows are aligned to that). Column sums stay in fp32 registers, are joined over the warps
+// through shared memory and over the row slices through the cluster's shared memory, always in the same
+// order. dx is the transposed product of tern_layer_gemm.cu on the rounded dz.
 #include "tern_layer.cuh"
 
 namespace tern {
 namespace {
 
-// One thread per output feature walks the rows: dz rounded to fp16, db summed unrounded in fp32.
-__global__ void __launch_bounds__(128) dz_kernel(const uint16_t* __restrict__ dy, const uint16_t* __restrict__ z,
-                                                 int64_t m, int64_t n, int act, int gated, uint16_t* dz, float* db) {
-  const int64_t nout = gated ? n / 2 : n;
-  const int64_t o = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  if (o >= nout) return;
-  double s0 = 0., s1 = 0.;
-  for (int64_t t = 0; t < m; t++) {
-    const float d = h2f(dy[t * nout + o]);
-    const float a = z ? h2f(z[t * n + o]) : 0.f;
-    if (gated) {
-      const float u = h2f(z[t * n + o + nout]);
-      const float g0 = d * u * act_bwd(act, a), g1 = d * act_fwd(act, a);
-      s0 += g0;
-      s1 += g1;
-      dz[t * n + o] = f2h(g0);
-      dz[t * n + o + nout] = f2h(g1);
-    } else {
-      const float g0 = d * act_bwd(act, a);
-      s0 += g0;
-      if (dz) dz[t * n + o] = f2h(g0);
-    }
+constexpr int kWarps = 8;
+
+struct DzParams {
+  const uint16_t *dy, *z;
+  uint16_t* dz;
+  float* db;
+  int64_t m, n, nout, dz_stride;
+  int act, gated, identity;
+};
+
+template <int VEC> struct Halves { uint16_t v[VEC]; };
+template <int VEC>
+__device__ __forceinline__ Halves<VEC> load_halves(const uint16_t* p) {
+  Halves<VEC> h;
+  if constexpr (VEC == 8) {
+    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+    *reinterpret_cast<uint4*>(h.v) = u;
+  } else {
+    h.v[0] = __ldcs(p);
   }
-  if (db) {
-    db[o] = (float)s0;
-    if (gated) db[o + nout] = (float)s1;
-  }
+  return h;
+}
+template <int VEC>
+__device__ __forceinline__ void store_halves(uint16_t* p, const Halves<VEC>& h) {
+  if constexpr (VEC == 8) *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(h.v);
+  else p[0] = h.v[0];
 }
 
-// One thread per column k and row of dz.
-__global__ void __launch_bounds__(128) dx_kernel(tern_matrix W, const uint16_t* __restrict__ dz, int64_t m, uint16_t* dx) {
-  const int64_t k = (int64_t)blockIdx.x * 128 + threadIdx.x;
-  const uint8_t* codes = static_cast<const uint8_t*>(W.codes);
-  for (int64_t t = blockIdx.y; t < m; t += gridDim.y) {
-    float acc = 0.f;
-    for (int64_t n = 0; n < W.n; n++)
-      acc = fmaf(h2f(dz[t * W.n + n]) * h2f(W.scales[n * W.scale_row_stride + blockIdx.x]),
-                 decode_t(W.layout, codes + n * W.code_row_stride, k), acc);
-    dx[t * W.k + k] = f2h(acc);
+__device__ __forceinline__ uint32_t cluster_rank_y() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_peer(const float* local, uint32_t rank) {
+  uint32_t remote;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"((uint32_t)__cvta_generic_to_shared(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+  return v;
+}
+
+template <int VEC>
+__global__ void __launch_bounds__(kWarps * 32) dz_kernel(const __grid_constant__ DzParams p) {
+  constexpr int kCols = 32 * VEC;
+  __shared__ float sums[2][kWarps][kCols];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t c = (int64_t)blockIdx.x * kCols + lane * VEC;
+  const int64_t r0 = p.m * blockIdx.y / gridDim.y, r1 = p.m * (blockIdx.y + 1) / gridDim.y;
+  float s0[VEC] = {}, s1[VEC] = {};
+  if (c < p.nout) {
+    for (int64_t t = r0 + warp; t < r1; t += kWarps) {
+      const Halves<VEC> d = load_halves<VEC>(p.dy + t * p.nout + c);
+      Halves<VEC> a{}, u{}, o0, o1;
+      if (!p.identity) a = load_halves<VEC>(p.z + t * p.n + c);
+      if (p.gated) u = load_halves<VEC>(p.z + t * p.n + p.nout + c);
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        const float g = h2f(d.v[i]), za = h2f(a.v[i]);
+        if (p.gated) {
+          float f, df;
+          act_both(p.act, za, &f, &df);
+          const float x0 = g * h2f(u.v[i]) * df, x1 = g * f;
+          s0[i] += x0;
+          s1[i] += x1;
+          o0.v[i] = f2h(x0);
+          o1.v[i] = f2h(x1);
+        } else {
+          const float x0 = p.identity ? g : g * act_bwd(p.act, za);
+          s0[i] += x0;
+          o0.v[i] = f2h(x0);
+        }
+      }
+      if (p.dz) {
+        store_halves<VEC>(p.dz + t * p.dz_stride + c, o0);
+        if (p.gated) store_halves<VEC>(p.dz + t * p.dz_stride + p.nout + c, o1);
+      }
+    }
   }
+  if (!p.db) return;  // the same for every CTA of the cluster
+#pragma unroll
+  for (int i = 0; i < VEC; i++) {
+    sums[0][warp][lane * VEC + i] = s0[i];
+    sums[1][warp][lane * VEC + i] = s1[i];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 2 * kCols; i += kWarps * 32) {
+    float s = 0.f;
+    for (int w = 0; w < kWarps; w++) s += sums[i / kCols][w][i % kCols];
+    sums[i / kCols][0][i % kCols] = s;  // only this thread reads and writes column i's sums
+  }
+  cluster_sync_all();
+  const uint32_t slices = gridDim.y;
+  for (int i = threadIdx.x + kWarps * 32 * (int)cluster_rank_y(); i < (p.gated ? 2 : 1) * kCols; i += kWarps * 32 * (int)slices) {
+    const int64_t j = (int64_t)blockIdx.x * kCols + i % kCols;
+    if (j >= p.nout) continue;
+    float s = 0.f;
+    for (uint32_t r = 0; r < slices; r++) s += ld_peer(&sums[i / kCols][0][i % kCols], r);
+    p.db[j + (i / kCols) * p.nout] = s;
+  }
+  cluster_sync_all();  // no CTA leaves while another may still read its sums
+}
+
+template <int VEC>
+cudaError_t launch_dz(const DzParams& p, cudaStream_t st) {
+  const int64_t cols = 32 * VEC;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((p.nout + cols - 1) / cols), p.m >= 64 ? 8 : p.m >= 16 ? 2 : 1);
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = cfg.gridDim.y;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, dz_kernel<VEC>, p);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_backward(const tern_matrix& W, const uint16_t* dy, const uint16_t* z, int64_t m, int act,
-                                   int gated, uint16_t* dx, uint16_t* dz, float* db, uint32_t* status, cudaStream_t st) {
-  (void)status;
-  const int64_t nout = gated ? W.n / 2 : W.n;
+                                   int gated, uint16_t* dx, uint16_t* dz, int64_t dz_stride, float* db, uint32_t* status,
+                                   cudaStream_t st) {
+  DzParams p{dy, z, dz, db, m, W.n, gated ? W.n / 2 : W.n, dz_stride, act, gated, act == TERN_ACT_NONE && !gated};
   if (dz || db) {
-    dz_kernel<<<(unsigned)((nout + 127) / 128), 128, 0, st>>>(dy, z, m, W.n, act, gated, dz, db);
-    const cudaError_t e = cudaGetLastError();
+    // 16-byte loads where every row of every operand starts on 16 bytes
+    const bool wide = p.nout % 8 == 0 && p.dz_stride % 8 == 0 &&
+                      ((reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(z) | reinterpret_cast<uintptr_t>(dz)) & 15u) == 0;
+    const cudaError_t e = wide ? launch_dz<8>(p, st) : launch_dz<1>(p, st);
     if (e != cudaSuccess) return e;
   }
   if (!dx) return cudaSuccess;
-  const dim3 grid((unsigned)(W.k / kGroup), (unsigned)std::min<int64_t>(m, 65535));
-  dx_kernel<<<grid, 128, 0, st>>>(W, dz ? dz : dy, m, dx);
-  return cudaGetLastError();
+  return dz ? launch_layer_gemm_t(W, dz, dz_stride, m, dx, status, st) : launch_layer_gemm_t(W, dy, W.n, m, dx, status, st);
 }
 
 }  // namespace tern

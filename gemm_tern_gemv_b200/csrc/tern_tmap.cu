@@ -45,6 +45,11 @@ using Key = std::tuple<const void*, int, uint64_t, uint64_t, uint64_t, uint32_t,
 
 }  // namespace
 
+bool tmap_2d_new(CUtensorMap* out, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
+                 uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
+  return make_map(out, dt, base, inner, outer, row_stride_bytes, box_inner, box_outer, sw);
+}
+
 bool tmap_2d(CUtensorMap* out, CUtensorMapDataType dt, const void* base, uint64_t inner, uint64_t outer,
              uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle sw) {
   static std::mutex mu;

@@ -366,14 +366,16 @@ TERN_API tern_status tern_linear(const tern_matrix* W, const uint16_t* x, int64_
  *   dy      device fp16 [m][n_out];  preact  device fp16 [m][n], what tern_linear stored (may be NULL
  *           for TERN_ACT_NONE without gating)
  *   dx      device fp16 [m][k] or NULL;  dbias  device fp32 [n] or NULL
- *   dz      device fp16 [m][n], 16-byte aligned; may be NULL for TERN_ACT_NONE without gating (dz is dy
- *           then, which must be 16-byte aligned), or when dx is NULL
+ *   dz      device fp16 [m][dz_row_stride], 16-byte aligned, dz_row_stride >= n a multiple of 8 (what lies
+ *           behind a row's n values is left as it was); may be NULL when dx is NULL, or for TERN_ACT_NONE
+ *           without gating with n a multiple of 8 (dz is dy then, which must be 16-byte aligned)
  *   outputs must not overlap the inputs or one another. Any m >= 1, any n. No workspace.
  * Errors: TERN_ERR_INVALID_ARG (also: all outputs NULL), TERN_ERR_UNSUPPORTED, TERN_ERR_ALIGNMENT,
  * TERN_ERR_CUDA. */
 TERN_API tern_status tern_linear_backward(const tern_matrix* W, const uint16_t* dy, const uint16_t* preact, int64_t m,
-                                          int32_t act, int32_t gated, uint16_t* dx, uint16_t* dz, float* dbias,
-                                          uint32_t* device_status, void* stream);
+                                          int32_t act, int32_t gated, uint16_t* dx, uint16_t* dz,
+                                          int64_t dz_row_stride, float* dbias, uint32_t* device_status,
+                                          void* stream);
 
 #define TERN_MOE_MAX_TOKENS 64
 #define TERN_MOE_MAX_EXPERTS 256

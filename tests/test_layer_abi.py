@@ -34,7 +34,7 @@ def _p(v):
 def test_bad_matrix(lib, kw, status):
     m, ok = _mat(**kw), _mat()
     assert lib.tern_linear(m, _p(FAKE), 1, _p(FAKE), None, 0, None, None) == status
-    assert lib.tern_linear_backward(m, _p(FAKE), None, 1, 0, 0, _p(FAKE), None, None, None, None) == status
+    assert lib.tern_linear_backward(m, _p(FAKE), None, 1, 0, 0, _p(FAKE), None, 0, None, None, None) == status
     for g, d in ((m, ok), (ok, m)):
         layer = T.TernMoeLayerC(ctypes.pointer(g), ctypes.pointer(d), FAKE, 4, 2, 3, 1)
         assert lib.tern_moe(layer, _p(FAKE), 1, None, _p(FAKE), None, None, _p(FAKE), 1 << 30, None, None) == status
@@ -61,11 +61,14 @@ def test_linear_rejects(lib):
 
 def test_linear_backward_rejects(lib):
     m = _mat()
-    f = lambda dy=FAKE, z=FAKE, rows=1, act=3, gated=0, dx=FAKE, dz=FAKE, db=FAKE, status=None: lib.tern_linear_backward(  # noqa: E731
-        m, _p(dy), _p(z), rows, act, gated, _p(dx), _p(dz), _p(db), _p(status), None)
+    f = lambda dy=FAKE, z=FAKE, rows=1, act=3, gated=0, dx=FAKE, dz=FAKE, stride=64, db=FAKE, status=None: lib.tern_linear_backward(  # noqa: E731
+        m, _p(dy), _p(z), rows, act, gated, _p(dx), _p(dz), stride, _p(db), _p(status), None)
     assert f(dy=0) == 1 and f(z=0) == 1 and f(rows=0) == 1 and f(gated=3) == 1 and f(act=9) == 2
     assert f(dx=0, dz=0, db=0) == 1 and f(dz=0) == 1  # dx needs dz once there is an activation
     assert f(act=0, dz=0, dy=FAKE + 2) == 3  # dz is dy: 16-byte aligned
+    assert f(stride=56) == 1 and f(stride=68) == 3
+    odd = _mat(n=63)
+    assert lib.tern_linear_backward(odd, _p(FAKE), None, 1, 0, 0, _p(FAKE), None, 0, None, None, None) == 1  # rows of dy unaligned
     assert f(dz=FAKE + 8) == 3 and f(dx=FAKE + 1) == 3 and f(db=FAKE + 2) == 3 and f(z=FAKE + 1) == 3 and f(status=FAKE + 1) == 3
 
 
