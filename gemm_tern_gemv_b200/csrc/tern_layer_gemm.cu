@@ -40,10 +40,9 @@ constexpr uint64_t kWaitNs = 1000000000ull;
 constexpr int X_BYTES = kMaxBN * BK * 2;
 constexpr int P_BYTES = BM * 32;  // codes of a stage: forward 128 rows x 16 or 32 bytes, transposed 64 x 16, 32 or 48
 constexpr int OFF_P = STAGES * X_BYTES;
-constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;  // transposed base-3: the two sets' tiles in Q2's form [64][32]
-constexpr int OFF_S = OFF_Q + 2 * 64 * 32;       // transposed: the two sets' 64 scales
-constexpr int OFF_LUT = OFF_S + 2 * 64 * 2;
-constexpr int OFF_BAR = OFF_LUT + 256 * 4;
+constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;  // transposed base-3: two tiles of each set in Q2's form [64][32]
+constexpr int OFF_LUT = OFF_Q + 4 * 64 * 32;
+constexpr int OFF_BAR = OFF_LUT + 256 * 32 * 4;
 constexpr int NUM_BARS = 2 * STAGES + 2 * ASTAGES + 4 + 1;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + slack to align the base to 1024
@@ -100,13 +99,25 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
       ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e != 0;
+}
 __device__ __forceinline__ void ldmatrix_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(addr)
                : "memory");
 }
-__device__ __forceinline__ void bar_sync(int id, int threads) { asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory"); }
+// Named barrier of `threads` threads; true if `fine` is true in all of them.
+__device__ __forceinline__ bool bar_all(int id, int threads, bool fine) {
+  uint32_t r = fine;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+               : "+r"(r) : "r"(id), "r"(threads) : "memory");
+  return r != 0;
+}
 
 // ---- decoding ------------------------------------------------------------------------------------------
 // fp16 pair s t from the pair's fp16 values 2 t: halved first, so that no scale can overflow.
@@ -126,14 +137,18 @@ __device__ __forceinline__ uint32_t pair_q1(uint32_t w, int p) {
   const uint32_t x = w & (3u << p);
   return ((x * ((1u << (15 - p)) + (1u << (30 - p)))) & 0x80008000u) ^ 0xBC00BC00u;
 }
-// 64 trits from digit R0 of p[0] on, as four words of 16 two's-complement fields.
-template <int R0>
-__device__ __forceinline__ void t3_words_r(const uint8_t* p, const uint32_t* lut, uint32_t (&w)[4]) {
-  constexpr int NB = (R0 + 63) / 5 + 1;
+// 64 trits as four words of 16 two's-complement fields. Trit 64 q starts at digit (64 q) mod 5 of byte
+// (64 q) / 5, which is 0, 12, 9, 6 or 3 past a 16-byte boundary for q mod 5 = V = 0 .. 4: u and v are the 32
+// bytes from that boundary on. lut: this lane's column of the table (32 copies, so that no two lanes of a warp
+// meet in a bank).
+template <int V>
+__device__ __forceinline__ void t3_words_v(const uint4& u, const uint4& v, const uint32_t* lut, uint32_t (&w)[4]) {
+  constexpr int kOff = (64 * V / 5) % 16, R0 = (64 * V) % 5, NB = (R0 + 63) / 5 + 1;
+  const uint32_t b[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
   w[0] = w[1] = w[2] = w[3] = 0;
 #pragma unroll
   for (int j = 0; j < NB; j++) {
-    const uint32_t f = lut[p[j]];
+    const uint32_t f = lut[__byte_perm(b[(kOff + j) >> 2], 0u, 0x4440 + ((kOff + j) & 3)) * 32u];
     const int at = 10 * j - 2 * R0;  // bit of the byte's first field
     if (at < 0) {
       w[0] |= f >> -at;
@@ -143,13 +158,14 @@ __device__ __forceinline__ void t3_words_r(const uint8_t* p, const uint32_t* lut
     }
   }
 }
-__device__ __forceinline__ void t3_words(int r0, const uint8_t* p, const uint32_t* lut, uint32_t (&w)[4]) {
-  switch (r0) {
-    case 0: t3_words_r<0>(p, lut, w); break;
-    case 1: t3_words_r<1>(p, lut, w); break;
-    case 2: t3_words_r<2>(p, lut, w); break;
-    case 3: t3_words_r<3>(p, lut, w); break;
-    default: t3_words_r<4>(p, lut, w); break;
+__device__ __forceinline__ void t3_words(int v5, const uint8_t* p, const uint32_t* lut, uint32_t (&w)[4]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p), v = *reinterpret_cast<const uint4*>(p + 16);
+  switch (v5) {
+    case 0: t3_words_v<0>(u, v, lut, w); break;
+    case 1: t3_words_v<1>(u, v, lut, w); break;
+    case 2: t3_words_v<2>(u, v, lut, w); break;
+    case 3: t3_words_v<3>(u, v, lut, w); break;
+    default: t3_words_v<4>(u, v, lut, w); break;
   }
 }
 
@@ -186,13 +202,14 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   }
   if (warp == 0 && lane == 0) { prefetch_tmap(&tmap_x); prefetch_tmap(&tmap_w); }
   if (LAYOUT == TERN_T3_5PB_G128) {
-    for (int v = threadIdx.x; v < 256; v += kThreads) {
+    for (int i = threadIdx.x; i < 256 * 32; i += kThreads) {
+      const int v = i / 32;
       uint32_t f = 0, r = (uint32_t)v;
       if (v < 243) {
 #pragma unroll
         for (int d = 0; d < 5; d++) { f |= ((r % 3u + 3u) & 3u) << (2 * d); r /= 3u; }  // c - 1 as two bits
       }
-      lut[v] = f;  // an invalid byte reads as five t = 0
+      lut[i] = f;  // an invalid byte reads as five t = 0
     }
   }
   if (warp == 1) {
@@ -244,43 +261,50 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16_f32(BM, p.bn);
-      uint32_t it = 0, lt = 0;
-      bool ok = true, issued = false;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, lt++) {
-        const uint32_t acc = lt & 1u;
-        if (!mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs)) {
+    // The whole warp runs the loop and one elected lane issues: the operands stay in uniform registers.
+    // (Issued from a branch that only one lane enters, every MMA took 94 cycles whatever its N; so it takes
+    // N / 2 + 11.)
+    const uint32_t idesc = idesc_f16_f32(BM, p.bn);
+    uint32_t it = 0, lt = 0;
+    bool ok = true, issued = false;
+    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, lt++) {
+      const uint32_t acc = lt & 1u;
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs))) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t tmem_d = tmem + acc * kMaxBN;
+      for (int kb = 0; kb < kblocks; kb++, it++) {
+        const int s = it % STAGES, d = it % ASTAGES;
+        bool fine = mbar_wait_bounded(full + s, (it / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        fine = fine && mbar_wait_bounded(dfull + d, (it / ASTAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        if (!__all_sync(0xffffffffu, fine)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t tmem_d = tmem + acc * kMaxBN;
-        for (int kb = 0; kb < kblocks; kb++, it++) {
-          const int s = it % STAGES, d = it % ASTAGES;
-          if (!mbar_wait_bounded(full + s, (it / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs) ||
-              !mbar_wait_bounded(dfull + d, (it / ASTAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint64_t bdesc = smem_desc_sw128(smem_u32(smem + s * X_BYTES));
-          const uint32_t a = tmem + kACol + d * 32;
+        const uint64_t bdesc = smem_desc_sw128(smem_u32(smem + s * X_BYTES));
+        const uint32_t a = tmem + kACol + d * 32;
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < BK / 16; kk++) mma_f16_ts(tmem_d, a + 8 * kk, bdesc + 2 * kk, idesc, (kb | kk) != 0);
-          issued = true;
           mma_commit(empty + s);
           mma_commit(dempty + d);
+          if (kb == kblocks - 1) mma_commit(tfull + acc);
         }
-        if (!ok) break;
-        mma_commit(tfull + acc);
+        __syncwarp();
+        issued = true;
       }
-      if (!ok && issued) {  // the MMAs already issued must end before tensor memory is freed
+    }
+    if (!ok && issued) {  // the MMAs already issued must end before tensor memory is freed
+      if (elect_one()) {
         mma_commit(drain);
         const uint64_t t0 = globaltimer_ns();
         while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs / 4) {
         }
       }
+      __syncwarp();
     }
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------------ epilogue
@@ -364,18 +388,20 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       const int64_t row = gated ? (int64_t)r0 + (src & 63) + (src >= 64 ? p.nout : 0) : (int64_t)r0 + src;
       const uint16_t* srow = p.scales + (row < p.n ? row : p.n - 1) * p.sstride;
       const int first = (int)((it ^ (uint32_t)set) & 1u);  // the set's first block of this tile
-      // transposed: thread st < 64 of the set brings the scale of one packed row; forward: the lane's own
-      auto fetch = [&](int kb) -> uint16_t {
+      // forward: the lane's own row's scale; transposed: those of packed rows 2 lane and 2 lane + 1 of the
+      // block as a pair
+      auto fetch = [&](int kb) -> uint32_t {
         if (kb >= kblocks) return 0;
         if (!TRANS) return __ldg(srow + (kb * BK) / kGroup);
-        const int64_t n = (int64_t)kb * BK + st;
-        return st < 64 && n < p.n ? __ldg(p.scales + n * p.sstride + r0 / kGroup) : (uint16_t)0;
+        const int64_t n = (int64_t)kb * BK + 2 * lane;
+        const uint16_t* q = p.scales + n * p.sstride + r0 / kGroup;
+        return (n < p.n ? (uint32_t)__ldg(q) : 0u) | (n + 1 < p.n ? (uint32_t)__ldg(q + p.sstride) << 16 : 0u);
       };
-      uint16_t sc = fetch(first);
+      uint32_t sc = fetch(first);
       for (int kb = first; kb < kblocks; kb += 2) {
         const uint32_t i = it + kb;
         const int s = i % STAGES, d = i % ASTAGES;
-        const uint16_t cur = sc;
+        const uint32_t cur = sc;
         sc = fetch(kb + 2);
         bool fine = mbar_wait_bounded(full + s, (i / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
         fine = fine && mbar_wait_bounded(dempty + d, ((i / ASTAGES) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
@@ -386,7 +412,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
             break;
           }
           tc_fence_after();
-          const __half2 s2 = __half2half2(__ushort_as_half(cur));
+          const __half2 s2 = __half2half2(__ushort_as_half((uint16_t)cur));
           uint32_t o[32];
           if (LAYOUT == TERN_Q1_0_G128) {
             const uint2 w = *reinterpret_cast<const uint2*>(P + src * 16 + 8 * (kb & 1));
@@ -402,42 +428,34 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
               const uint4 u = *reinterpret_cast<const uint4*>(P + src * 16);
               w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
             } else {
-              const int t0 = kb * BK;
-              t3_words(t0 % 5, P + src * 32 + ((t0 / 5) & 15), lut, w);
+              t3_words(kb % 5, P + src * 32, lut + lane, w);
             }
 #pragma unroll
             for (int j = 0; j < 32; j++) o[j] = scaled(pair_q2(w[j >> 3], j & 7), s2);
           }
           tmem_st_32x32b_x32(a_lane + d * 32, o);
         } else {
-          // scales (and base-3 words) of the block are shared by the set's four warps, which all leave together
-          uint16_t* S = reinterpret_cast<uint16_t*>(smem + OFF_S) + set * 64;
-          uint8_t* Q = smem + OFF_Q + set * 64 * 32;
-          bar_sync(1 + set, 128);  // the set is done with the block before
-          if (st < 64) S[st] = cur;
-          if (!fine) *abort_flag = 1;
-          if (LAYOUT == TERN_T3_5PB_G128 && fine) {
-            const int t0 = r0 + 64 * (st & 1);
-            uint32_t w[4];
-            t3_words(t0 % 5, P + (st >> 1) * 48 + t0 / 5 - ((r0 / 5) & ~15), lut, w);
-            *reinterpret_cast<uint4*>(Q + (st >> 1) * 32 + 16 * (st & 1)) = make_uint4(w[0], w[1], w[2], w[3]);
+          const uint32_t Q = smem_u32(smem + OFF_Q + (set * 2 + ((i >> 1) & 1)) * 64 * 32);
+          if (LAYOUT == TERN_T3_5PB_G128) {
+            // the set's four warps write the block in Q2's form for one another, into two buffers in turn: who
+            // has passed this block's barrier has done with the buffer of the block before
+            if (fine) {
+              const int t0 = r0 + (st & 64);  // two warps take the first 64 columns of the 64 rows, two the others
+              uint32_t w[4];
+              t3_words((t0 / 64) % 5, P + (st & 63) * 48 + (((t0 / 5) & ~15) - ((r0 / 5) & ~15)), lut + lane, w);
+              *reinterpret_cast<uint4*>(smem + OFF_Q + (set * 2 + ((i >> 1) & 1)) * 64 * 32 + (st & 63) * 32 + (st & 64 ? 16 : 0)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fine = bar_all(1 + set, 128, fine);  // the four warps leave together
           }
-          bar_sync(1 + set, 128);
-          if (*abort_flag) fine = false;
-          // the verdict is the same in all four warps: the flag is raised before the barrier above or by
-          // others at any time, so it is agreed on once more
-          fine = __all_sync(0xffffffffu, fine);
-          int all = fine ? 1 : 0;
-          asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %0, 0;\n\tbar.red.and.pred q, %1, 128, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
-                       : "+r"(all) : "r"(1 + set) : "memory");
-          if (!all) {
+          if (!__all_sync(0xffffffffu, fine)) {
             ok = false;
             break;
           }
           tc_fence_after();
           // columns of 16 bits of the codes: Q2 eight fields (two column groups of 16 bytes), binary 16 bits
           const int group = LAYOUT == TERN_Q1_0_G128 ? 0 : quad >> 1;
-          const uint32_t base = LAYOUT == TERN_T3_5PB_G128 ? smem_u32(Q) : smem_u32(P);
+          const uint32_t base = LAYOUT == TERN_T3_5PB_G128 ? Q : smem_u32(P);
           constexpr int pitch = LAYOUT == TERN_Q1_0_G128 ? 16 : 32;
           uint32_t R[8], sp[8];
 #pragma unroll
@@ -448,7 +466,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
             for (int q = 0; q < 4; q++) R[4 * h + q] = v[q];
           }
 #pragma unroll
-          for (int q = 0; q < 8; q++) sp[q] = *reinterpret_cast<const uint32_t*>(S + 8 * q + 2 * (lane & 3));
+          for (int q = 0; q < 8; q++) sp[q] = __shfl_sync(0xffffffffu, cur, 4 * q + (lane & 3));
           const int f0 = LAYOUT == TERN_Q1_0_G128 ? 4 * quad : 4 * (quad & 1);  // the warp's first field
           const uint32_t up_mul = LAYOUT == TERN_Q1_0_G128 ? 1u << (12 - f0) : 1u << (8 - 2 * f0);
 #pragma unroll
@@ -512,15 +530,15 @@ cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, P
   return cudaGetLastError();
 }
 
-// Rows of x per tile: the multiple of 16 up to kMaxBN that makes the waves of tiles cheapest. A tile costs
-// its columns plus what does not shrink with them (the decoding of A, about 64 columns' worth of MMAs).
+// Rows of x per tile: the multiple of 16 up to kMaxBN that makes the waves of tiles cheapest. 64 terms of a
+// tile cost four MMAs of bn / 2 + 11 cycles (measured), and no less than their decoding (about 290).
 int pick_bn(int64_t m, int64_t rtiles, int sms) {
   int best = kMaxBN;
   double cost = -1;
   for (int bn = 16; bn <= kMaxBN; bn += 16) {
     if (bn > 16 && bn - 16 >= m) break;
     const int64_t tiles = rtiles * ((m + bn - 1) / bn), waves = (tiles + sms - 1) / sms;
-    const double c = (double)waves * std::max(bn, 96);
+    const double c = (double)waves * std::max(2 * bn + 44, 290);
     if (cost < 0 || c <= cost) {
       cost = c;
       best = bn;
