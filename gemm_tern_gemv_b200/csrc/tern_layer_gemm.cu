@@ -2,15 +2,19 @@
 //     forward     z[t][n]  = sum_k x[t][k]  s[n][k/128] t[n][k]     (tern_linear)
 //     transposed  dx[t][k] = sum_n dz[t][n] s[n][k/128] t[n][k]     (tern_linear_backward)
 //
-// A CTA computes tiles of 128 weight rows (forward) or weight columns (transposed) by `bn` rows of x, 64
-// terms of the sum at a time. In D = A B^T the decoded weights are A (M = 128), the activations B.
-//   * What bounds it. Per 64 terms the MMAs take bn / 256 x 512 cycles; B is written to shared memory by
-//     TMA and read by the MMAs, together 128 bytes a cycle at the MMAs' full rate, which is all that
-//     shared memory gives. So A must not go through it too: it lives in tensor memory. Decoder warps turn
-//     codes into fp16 s t in registers (exact) and store them with tcgen05.st; 32 columns hold 64 terms.
+// A pair of CTAs computes tiles of 256 weight rows (forward) or weight columns (transposed), 128 in each, by
+// `bn` rows of x, 64 terms of the sum at a time. In D = A B^T the decoded weights are A (cta_group::2,
+// M = 256), the activations B.
+//   * What bounds it. Per 64 terms the MMAs take bn / 256 x 512 cycles. With one CTA a tile, B would be
+//     written to shared memory by TMA and read by the MMAs at 128 bytes a cycle in all, which is all that
+//     shared memory gives, and would cross from L2 at 64 bytes a cycle and SM, more than L2 gives (a version
+//     of this kernel without pairs stopped at 0.9 PFLOP/s there). As a pair each CTA brings half of B. And
+//     A does not go through shared memory at all, it lives in tensor memory: decoder warps turn codes into
+//     fp16 s t in registers (exact) and store them with tcgen05.st; 32 columns hold 64 terms.
 //   * Tensor memory: two accumulators of up to 192 columns, so that the epilogue of a tile runs beside the
-//     MMAs of the next, and a ring of four A stages (4 x 32 columns).
-//   * Warps: 0 TMA, 1 MMA, 4-7 epilogue, 8-15 decode (two sets of four; a set takes every other 64 terms).
+//     MMAs of the next, and a ring of 4 to 8 A stages of 32 columns in what they leave.
+//   * Warps: 0 and 2 TMA, 1 MMA, 4-7 epilogue, 8 on decode (four sets of four; a set takes every fourth stage,
+//     which hides the latencies between a stage's arrival and its decoded weights').
 //   * bn is chosen by the host so that the tiles fill whole waves of CTAs.
 //   * Transposed: A's rows are the columns of the packed rows, whose group is one scale per packed row.
 //     ldmatrix.trans hands a lane 16-bit pieces of two adjacent rows; each field of theirs is a finished
@@ -30,18 +34,19 @@ using namespace sm100;
 
 constexpr int BM = 128;      // rows of A per tile
 constexpr int BK = 64;       // terms per stage (one 128-byte swizzle row of fp16)
-constexpr int kMaxBN = 192;  // rows of x per tile
-constexpr int STAGES = 6;    // TMA ring
-constexpr int ASTAGES = 4;   // A ring in tensor memory
-constexpr int kThreads = 512;
-constexpr uint32_t kTmemCols = 512, kACol = 2 * kMaxBN;  // accumulators at 0 and kMaxBN, A from kACol
+constexpr int kMaxBN = 192;  // rows of x per tile (of a pair of CTAs)
+constexpr int STAGES = 8;    // TMA ring
+constexpr int ASTAGES = 8;   // A ring in tensor memory, at most: what the accumulators leave of it
+constexpr int SETS = 4;      // sets of four decoder warps; a set takes every SETS-th stage
+constexpr int kThreads = 256 + SETS * 128;
+constexpr uint32_t kTmemCols = 512;  // accumulators at 0 and bn, the A ring from 2 bn on
 constexpr uint64_t kWaitNs = 1000000000ull;
 
-constexpr int X_BYTES = kMaxBN * BK * 2;
+constexpr int X_BYTES = kMaxBN / 2 * BK * 2;  // a CTA's half of the tile's rows of x
 constexpr int P_BYTES = BM * 32;  // codes of a stage: forward 128 rows x 16 or 32 bytes, transposed 64 x 16, 32 or 48
 constexpr int OFF_P = STAGES * X_BYTES;
 constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;  // transposed base-3: two tiles of each set in Q2's form [64][32]
-constexpr int OFF_LUT = OFF_Q + 4 * 64 * 32;
+constexpr int OFF_LUT = OFF_Q + 2 * SETS * 64 * 32;
 constexpr int OFF_BAR = OFF_LUT + 256 * 32 * 4;
 constexpr int NUM_BARS = 2 * STAGES + 2 * ASTAGES + 4 + 1;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
@@ -95,9 +100,52 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uin
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
       ::"r"(tmem_d), "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// ---- pairs of CTAs ------------------------------------------------------------------------------------
+__device__ __forceinline__ void tmem_alloc_pair(uint32_t* dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void tmem_relinquish_pair() {
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+// Arrives on `bar` of both CTAs once every MMA issued before has completed.
+__device__ __forceinline__ void commit_both(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+               ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+}
+__device__ __forceinline__ void commit_own(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Arrives on the first CTA's copy of `bar`.
+__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+  uint32_t remote;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_u32(bar)));
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+// Waits on a barrier that both CTAs arrive on.
+__device__ __forceinline__ bool try_wait_pair(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity) : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* status) {
+  return mbar_wait_bounded(bar, parity, abort, status, TERN_DEVICE_TIMEOUT, kWaitNs) && try_wait_pair(bar, parity);
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -171,7 +219,7 @@ __device__ __forceinline__ void t3_words(int v5, const uint8_t* p, const uint32_
 
 // ---- the kernel ------------------------------------------------------------------------------------------
 template <int LAYOUT, bool TRANS>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -187,15 +235,17 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   uint32_t* lut = reinterpret_cast<uint32_t*>(smem + OFF_LUT);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int tiles = p.rtiles * p.mtiles;
+  const int rank = (int)cluster_rank(), pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+  const int tiles = (p.rtiles + 1) / 2 * p.mtiles;  // of pairs
   const int kblocks = (p.terms + BK - 1) / BK;
+  const uint32_t a_col = 2 * p.bn, a_stages = min((kTmemCols - a_col) / 32, (uint32_t)ASTAGES);
   const bool gated = !TRANS && p.e.gated;
   const int step = gated ? 64 : BM;  // outputs of a tile
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; i++) { mbar_init(full + i, 1); mbar_init(empty + i, 1); }
-    for (int i = 0; i < ASTAGES; i++) { mbar_init(dfull + i, 4); mbar_init(dempty + i, 1); }
-    for (int i = 0; i < 2; i++) { mbar_init(tfull + i, 1); mbar_init(tempty + i, 4); }
+    for (int i = 0; i < STAGES; i++) { mbar_init(full + i, 2); mbar_init(empty + i, 1); }
+    for (int i = 0; i < ASTAGES; i++) { mbar_init(dfull + i, 8); mbar_init(dempty + i, 1); }
+    for (int i = 0; i < 2; i++) { mbar_init(tfull + i, 1); mbar_init(tempty + i, 8); }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -213,99 +263,106 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     }
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, kTmemCols);
-    tmem_relinquish();
+    tmem_alloc_pair(tmem_holder, kTmemCols);
+    tmem_relinquish_pair();
   }
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // both CTAs' barriers are ready before either arrives on the other's
   tc_fence_after();
-  const uint32_t tmem = *tmem_holder;
+  const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_holder);  // the same in all lanes, in a uniform register
 
-  if (warp == 0) {
-    // ------------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      constexpr int P_ROW = TRANS ? (LAYOUT == TERN_Q1_0_G128 ? 16 : LAYOUT == TERN_Q2_0_G128 ? 32 : 48)
-                                  : (LAYOUT == TERN_T3_5PB_G128 ? 32 : 16);
-      const uint32_t bytes = (uint32_t)p.bn * BK * 2 + (TRANS ? BK : BM) * P_ROW;
-      for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-        const int r0 = (tile / p.mtiles) * step, m0 = (tile % p.mtiles) * p.bn;
-        for (int kb = 0; kb < kblocks; kb++, it++) {
-          const int s = it % STAGES;
-          if (!mbar_wait_bounded(empty + s, ((it / STAGES) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs)) {
-            ok = false;
-            break;
-          }
+  if (warp == 0 || warp == 2) {
+    // ------------------------------------------------------------------ TMA producers
+    // Warp 0 brings the rows of x, warp 2 the codes. As in the MMA warp the whole warp runs the loop and one
+    // elected lane issues (one lane's loop with both took 600 cycles a stage, more than the MMAs).
+    constexpr int P_ROW = TRANS ? (LAYOUT == TERN_Q1_0_G128 ? 16 : LAYOUT == TERN_Q2_0_G128 ? 32 : 48)
+                                : (LAYOUT == TERN_T3_5PB_G128 ? 32 : 16);
+    const uint32_t bytes = warp == 0 ? (uint32_t)p.bn / 2 * BK * 2 : (TRANS ? BK : BM) * P_ROW;
+    uint32_t ph = 1;
+    int s = 0, sent = 0;
+    bool dead = false;
+    for (int tile = pair; tile < tiles; tile += pairs) {
+      const int r0 = (tile / p.mtiles * 2 + rank) * step, m0 = (tile % p.mtiles) * p.bn + rank * (p.bn / 2);
+      for (int kb = 0; kb < kblocks; kb++) {
+        if (!dead) dead = !mbar_wait_bounded(empty + s, ph, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        dead = __any_sync(0xffffffffu, dead);
+        if (elect_one() && !dead) {
           mbar_arrive_expect_tx(full + s, bytes);
-          tma_load_2d(smem + s * X_BYTES, &tmap_x, full + s, kb * BK, m0);
-          uint8_t* dst = smem + OFF_P + s * P_BYTES;
-          if (TRANS) {  // columns r0 .. r0 + 127 of rows kb * 64 ..
-            const int px = LAYOUT == TERN_Q2_0_G128 ? r0 / 4 : LAYOUT == TERN_Q1_0_G128 ? r0 / 8 : (r0 / 5) & ~15;
-            tma_load_2d(dst, &tmap_w, full + s, px, kb * BK);
+          if (warp == 0) {
+            tma_load_2d(smem + s * X_BYTES, &tmap_x, full + s, kb * BK, m0);
           } else {
-            const int px = LAYOUT == TERN_Q2_0_G128 ? kb * (BK / 4) : LAYOUT == TERN_Q1_0_G128 ? (kb * (BK / 8)) & ~15 : ((kb * BK) / 5) & ~15;
-            tma_load_2d(dst, &tmap_w, full + s, px, r0);
-            if (gated) tma_load_2d(dst + 64 * P_ROW, &tmap_w, full + s, px, (int)p.nout + r0);
+            uint8_t* dst = smem + OFF_P + s * P_BYTES;
+            if (TRANS) {  // columns r0 .. r0 + 127 of rows kb * 64 ..
+              const int px = LAYOUT == TERN_Q2_0_G128 ? r0 / 4 : LAYOUT == TERN_Q1_0_G128 ? r0 / 8 : (r0 / 5) & ~15;
+              tma_load_2d(dst, &tmap_w, full + s, px, kb * BK);
+            } else {
+              const int px = LAYOUT == TERN_Q2_0_G128 ? kb * (BK / 4) : LAYOUT == TERN_Q1_0_G128 ? (kb * (BK / 8)) & ~15 : ((kb * BK) / 5) & ~15;
+              tma_load_2d(dst, &tmap_w, full + s, px, r0);
+              if (gated) tma_load_2d(dst + 64 * P_ROW, &tmap_w, full + s, px, (int)p.nout + r0);
+            }
           }
-        }
-      }
-      // copies in flight must land before the CTA's shared memory goes away (the last round's are waited
-      // for by the decoders unless they gave up)
-      if (!ok) {
-        const uint64_t t0 = globaltimer_ns();
-        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; i++)
-          while (!mbar_try_wait(full + i % STAGES, (i / STAGES) & 1u) && globaltimer_ns() - t0 < kWaitNs / 4) {
-          }
-      }
-    }
-  } else if (warp == 1) {
-    // ------------------------------------------------------------------ MMA issuer
-    // The whole warp runs the loop and one elected lane issues: the operands stay in uniform registers.
-    // (Issued from a branch that only one lane enters, every MMA took 94 cycles whatever its N; so it takes
-    // N / 2 + 11.)
-    const uint32_t idesc = idesc_f16_f32(BM, p.bn);
-    uint32_t it = 0, lt = 0;
-    bool ok = true, issued = false;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x, lt++) {
-      const uint32_t acc = lt & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs))) {
-        ok = false;
-        break;
-      }
-      tc_fence_after();
-      const uint32_t tmem_d = tmem + acc * kMaxBN;
-      for (int kb = 0; kb < kblocks; kb++, it++) {
-        const int s = it % STAGES, d = it % ASTAGES;
-        bool fine = mbar_wait_bounded(full + s, (it / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
-        fine = fine && mbar_wait_bounded(dfull + d, (it / ASTAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
-        if (!__all_sync(0xffffffffu, fine)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint64_t bdesc = smem_desc_sw128(smem_u32(smem + s * X_BYTES));
-        const uint32_t a = tmem + kACol + d * 32;
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < BK / 16; kk++) mma_f16_ts(tmem_d, a + 8 * kk, bdesc + 2 * kk, idesc, (kb | kk) != 0);
-          mma_commit(empty + s);
-          mma_commit(dempty + d);
-          if (kb == kblocks - 1) mma_commit(tfull + acc);
         }
         __syncwarp();
-        issued = true;
-      }
-    }
-    if (!ok && issued) {  // the MMAs already issued must end before tensor memory is freed
-      if (elect_one()) {
-        mma_commit(drain);
-        const uint64_t t0 = globaltimer_ns();
-        while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs / 4) {
+        if (!dead) sent++;
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
         }
       }
-      __syncwarp();
     }
+    // copies in flight must land before the CTA's shared memory goes away. (Otherwise the decoders have waited
+    // for them all.) A stage's barrier completes only if both warps sent theirs, so this wait is bounded too.
+    if (dead && lane == 0) {
+      const uint64_t t0 = globaltimer_ns();
+      for (int i = sent > STAGES ? sent - STAGES : 0; i < sent; i++)
+        while (!mbar_try_wait(full + i % STAGES, (uint32_t)(i / STAGES) & 1u) && globaltimer_ns() - t0 < kWaitNs / 4) {
+        }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ------------------------------------------------------------------ MMA issuer
+    // The whole warp runs the loop, without leaving it early, and one elected lane issues: so the operands
+    // stay in uniform registers. (Where the loop can be left on a wait's verdict, or is run by one lane, every
+    // MMA takes about 100 cycles whatever its N; as it is, N / 2 + 11.)
+    const uint32_t idesc = idesc_f16_f32(2 * BM, p.bn);
+    uint32_t lt = 0, dph = 0;
+    int s = 0, d = 0;
+    bool dead = false, issued = false, ready = false;
+    for (int tile = pair; tile < tiles; tile += pairs, lt++) {
+      const uint32_t acc = lt & 1u;
+      if (!dead) dead = !mbar_wait_bounded(tempty + acc, ((lt >> 1) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+      const uint32_t tmem_d = tmem + acc * p.bn;
+      for (int kb = 0; kb < kblocks; kb++) {
+        // both CTAs' decoders arrive after their A is stored, and after they saw their stage's copies land
+        if (!dead && !ready) dead = !wait_pair(dfull + d, dph, abort_flag, p.status);
+        dead = __any_sync(0xffffffffu, dead);
+        tc_fence_after();
+        const uint64_t bdesc = smem_desc_sw128(smem_u32(smem + s * X_BYTES));
+        const uint32_t a = tmem + a_col + d * 32;
+        if (elect_one() && !dead) {
+#pragma unroll
+          for (int kk = 0; kk < BK / 16; kk++) mma_f16_ts(tmem_d, a + 8 * kk, bdesc + 2 * kk, idesc, (kb | kk) != 0);
+          commit_both(empty + s);
+          commit_both(dempty + d);
+          if (kb == kblocks - 1) commit_both(tfull + acc);
+          issued = true;
+        }
+        __syncwarp();
+        if (++s == STAGES) s = 0;
+        if (++d == (int)a_stages) {
+          d = 0;
+          dph ^= 1u;
+        }
+        ready = try_wait_pair(dfull + d, dph);  // looked at while the MMAs run
+      }
+    }
+    if (dead && issued) {  // (in the lane that issued) the MMAs must end before tensor memory is freed
+      commit_own(drain);
+      const uint64_t t0 = globaltimer_ns();
+      while (!mbar_try_wait(drain, 0) && globaltimer_ns() - t0 < kWaitNs / 4) {
+      }
+    }
+    __syncwarp();
   } else if (warp >= 4 && warp < 8) {
     // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3;
@@ -316,15 +373,15 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     else if (LAYOUT == TERN_Q1_0_G128) o = 16 * (lane & 7) + 4 * quad + (lane >> 3);
     else o = 64 * (quad >> 1) + 8 * (lane & 7) + 4 * (quad & 1) + (lane >> 3);
     uint32_t lt = 0;
-    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, lt++) {
-      const int64_t j = (int64_t)(tile / p.mtiles) * step + o;  // output column
+    for (int tile = pair; tile < tiles; tile += pairs, lt++) {
+      const int64_t j = (int64_t)(tile / p.mtiles * 2 + rank) * step + o;  // output column
       const int64_t m0 = (int64_t)(tile % p.mtiles) * p.bn;
       const bool in = j < p.nout;
       const float bias = !TRANS && p.e.bias && in ? h2f(p.e.bias[j + (up ? p.nout : 0)]) : 0.f;
       const uint32_t acc = lt & 1u;
       if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs))) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + acc * kMaxBN + ((uint32_t)(quad * 32) << 16);
+      const uint32_t taddr = tmem + acc * p.bn + ((uint32_t)(quad * 32) << 16);
       const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);  // rows of x in this tile
 #pragma unroll 1
       for (int c0 = 0; c0 < cols; c0 += 16) {
@@ -373,38 +430,38 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(tempty + acc);
+      if (lane == 0) arrive_first(tempty + acc);
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ decoders
     const int quad = warp & 3, set = (warp - 8) >> 2, st = threadIdx.x & 127;
-    const uint32_t a_lane = tmem + kACol + ((uint32_t)(quad * 32) << 16);
-    uint32_t it = 0;
+    const uint32_t a_lane = tmem + a_col + ((uint32_t)(quad * 32) << 16);
+    // stage and A slot of the set's next block, with the parities to wait for
+    int s = set % STAGES, d = set % (int)a_stages, kb = set, flip = 0;
+    uint32_t fph = 0, eph = 1;
     bool ok = true;
-    for (int tile = blockIdx.x; tile < tiles && ok; tile += gridDim.x) {
-      const int r0 = (tile / p.mtiles) * step;
+    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+      const int r0 = (tile / p.mtiles * 2 + rank) * step;
       // forward: this lane's row of A is packed row `row`, at row `src` of the stage's codes
       const int src = gated ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
       const int64_t row = gated ? (int64_t)r0 + (src & 63) + (src >= 64 ? p.nout : 0) : (int64_t)r0 + src;
       const uint16_t* srow = p.scales + (row < p.n ? row : p.n - 1) * p.sstride;
-      const int first = (int)((it ^ (uint32_t)set) & 1u);  // the set's first block of this tile
       // forward: the lane's own row's scale; transposed: those of packed rows 2 lane and 2 lane + 1 of the
       // block as a pair
       auto fetch = [&](int kb) -> uint32_t {
-        if (kb >= kblocks) return 0;
+        if (kb >= kblocks || (TRANS && r0 >= p.k)) return 0;  // (the second CTA's columns may lie past the matrix)
         if (!TRANS) return __ldg(srow + (kb * BK) / kGroup);
         const int64_t n = (int64_t)kb * BK + 2 * lane;
         const uint16_t* q = p.scales + n * p.sstride + r0 / kGroup;
         return (n < p.n ? (uint32_t)__ldg(q) : 0u) | (n + 1 < p.n ? (uint32_t)__ldg(q + p.sstride) << 16 : 0u);
       };
-      uint32_t sc = fetch(first);
-      for (int kb = first; kb < kblocks; kb += 2) {
-        const uint32_t i = it + kb;
-        const int s = i % STAGES, d = i % ASTAGES;
+      uint32_t sc = fetch(kb);
+      for (; kb < kblocks; kb += SETS) {
         const uint32_t cur = sc;
-        sc = fetch(kb + 2);
-        bool fine = mbar_wait_bounded(full + s, (i / STAGES) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
-        fine = fine && mbar_wait_bounded(dempty + d, ((i / ASTAGES) & 1u) ^ 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        const bool f0 = mbar_try_wait(full + s, fph), e0 = mbar_try_wait(dempty + d, eph);
+        sc = fetch(kb + SETS);
+        bool fine = f0 || mbar_wait_bounded(full + s, fph, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+        fine = fine && (e0 || mbar_wait_bounded(dempty + d, eph, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs));
         const uint8_t* P = smem + OFF_P + s * P_BYTES;
         if constexpr (!TRANS) {
           if (!__all_sync(0xffffffffu, fine)) {
@@ -435,7 +492,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
           }
           tmem_st_32x32b_x32(a_lane + d * 32, o);
         } else {
-          const uint32_t Q = smem_u32(smem + OFF_Q + (set * 2 + ((i >> 1) & 1)) * 64 * 32);
+          const uint32_t Q = smem_u32(smem + OFF_Q + (set * 2 + flip) * 64 * 32);
           if (LAYOUT == TERN_T3_5PB_G128) {
             // the set's four warps write the block in Q2's form for one another, into two buffers in turn: who
             // has passed this block's barrier has done with the buffer of the block before
@@ -443,7 +500,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
               const int t0 = r0 + (st & 64);  // two warps take the first 64 columns of the 64 rows, two the others
               uint32_t w[4];
               t3_words((t0 / 64) % 5, P + (st & 63) * 48 + (((t0 / 5) & ~15) - ((r0 / 5) & ~15)), lut + lane, w);
-              *reinterpret_cast<uint4*>(smem + OFF_Q + (set * 2 + ((i >> 1) & 1)) * 64 * 32 + (st & 63) * 32 + (st & 64 ? 16 : 0)) =
+              *reinterpret_cast<uint4*>(smem + OFF_Q + (set * 2 + flip) * 64 * 32 + (st & 63) * 32 + (st & 64 ? 16 : 0)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
             fine = bar_all(1 + set, 128, fine);  // the four warps leave together
@@ -495,17 +552,25 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(dfull + d);
+        if (lane == 0) arrive_first(dfull + d);
+        flip ^= 1;
+        s += SETS;
+        if (s >= STAGES) {
+          s -= STAGES;
+          fph ^= 1u;
+        }
+        for (d += SETS; d >= (int)a_stages; d -= (int)a_stages) eph ^= 1u;
       }
-      it += kblocks;
+      kb -= kblocks;
     }
   }
 
   tc_fence_before();
   __syncthreads();
+  cluster_sync();  // neither CTA leaves while the other may still arrive on its barriers or read its operands
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmemCols);
+    tmem_dealloc_pair(tmem, kTmemCols);
   }
 }
 
@@ -513,7 +578,7 @@ template <int LAYOUT, bool TRANS>
 cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, Params& p, cudaStream_t st) {
   CUtensorMap mx, mw;
   if (!tmap_2d_new(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)p.terms, (uint64_t)p.m, (uint64_t)xstride * 2, BK,
-                   (uint32_t)p.bn, CU_TENSOR_MAP_SWIZZLE_128B))
+                   (uint32_t)p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
   // codes as bytes [n][row data]: reads past them give zero
   const uint64_t data = LAYOUT == TERN_Q2_0_G128 ? W.k / 4 : LAYOUT == TERN_Q1_0_G128 ? W.k / 8 : (W.k + 4) / 5;
@@ -525,19 +590,19 @@ cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, P
   const void* kern = reinterpret_cast<const void*>(&layer_gemm_kernel<LAYOUT, TRANS>);
   const cudaError_t e = allow_smem(kern, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (int64_t)p.rtiles * p.mtiles;
-  layer_gemm_kernel<LAYOUT, TRANS><<<(unsigned)std::min<int64_t>(tiles, sm_count()), kThreads, SMEM_BYTES, st>>>(mx, mw, p);
+  const int64_t tiles = ((int64_t)p.rtiles + 1) / 2 * p.mtiles;
+  layer_gemm_kernel<LAYOUT, TRANS><<<(unsigned)std::min<int64_t>(tiles, sm_count() / 2) * 2, kThreads, SMEM_BYTES, st>>>(mx, mw, p);
   return cudaGetLastError();
 }
 
-// Rows of x per tile: the multiple of 16 up to kMaxBN that makes the waves of tiles cheapest. 64 terms of a
+// Rows of x per tile: the multiple of 32 up to kMaxBN that makes the waves of tiles cheapest. 64 terms of a
 // tile cost four MMAs of bn / 2 + 11 cycles (measured), and no less than their decoding (about 290).
 int pick_bn(int64_t m, int64_t rtiles, int sms) {
   int best = kMaxBN;
   double cost = -1;
-  for (int bn = 16; bn <= kMaxBN; bn += 16) {
-    if (bn > 16 && bn - 16 >= m) break;
-    const int64_t tiles = rtiles * ((m + bn - 1) / bn), waves = (tiles + sms - 1) / sms;
+  for (int bn = 32; bn <= kMaxBN; bn += 32) {
+    if (bn > 32 && bn - 32 >= m) break;
+    const int64_t tiles = (rtiles + 1) / 2 * ((m + bn - 1) / bn), waves = (tiles + sms / 2 - 1) / (sms / 2);
     const double c = (double)waves * std::max(2 * bn + 44, 290);
     if (cost < 0 || c <= cost) {
       cost = c;
