@@ -27,13 +27,16 @@ __device__ __forceinline__ uint16_t f2h(float f) { return __half_as_ushort(__flo
 // is z sigmoid(u), u = sqrt(8 / pi) (z + 0.044715 z^3), since (1 + tanh(u / 2)) / 2 = sigmoid(u).
 __device__ __forceinline__ float gelu_tanh_u(float z) { return 1.5957691216057308f * (z + 0.044715f * z * z * z); }
 
+// Out of line: inlined many times over it would cost the epilogues their registers.
+static __device__ __noinline__ float gelu_erf(float z) { return 0.5f * z * erfcf(-0.70710678118654752f * z); }
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
     case TERN_ACT_RELU: return z < 0.f ? 0.f : z;  // NaN stays NaN
     case TERN_ACT_RELU2: return z < 0.f ? 0.f : z * z;
     case TERN_ACT_SILU:
     case TERN_ACT_GELU_TANH: return __fdividef(z, 1.f + __expf(act == TERN_ACT_SILU ? -z : -gelu_tanh_u(z)));
-    case TERN_ACT_GELU: return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case TERN_ACT_GELU: return gelu_erf(z);
     default: return z;
   }
 }
@@ -57,17 +60,33 @@ __device__ __forceinline__ float act_bwd(int act, float z) {
   }
 }
 
-// act(z) and act'(z) together.
+// act(z) and act'(z) together. The fast exponential and division are off by a few units of 2^-24 times
+// (1 + |u|), far below the rounding to fp16 that follows.
 __device__ __forceinline__ void act_both(int act, float z, float* f, float* df) {
   if (act == TERN_ACT_SILU || act == TERN_ACT_GELU_TANH) {
     const float u = act == TERN_ACT_SILU ? z : gelu_tanh_u(z);
-    const float s = 1.f / (1.f + expf(-u)), c = 1.f / (1.f + expf(u));
+    // sigmoid s = 1 / (1 + e^-u) and its complement e^-u s; past e^80 both products with z vanish in fp32 alike
+    const float e = __expf(fminf(-u, 80.f)), s = __fdividef(1.f, 1.f + e), c = e * s;
     const float du = act == TERN_ACT_SILU ? 1.f : 1.5957691216057308f * (1.f + 0.134145f * z * z);
     *f = z * s;
     *df = s + z * s * c * du;
   } else {
     *f = act_fwd(act, z);
     *df = act_bwd(act, z);
+  }
+}
+
+// f called with the activation as a compile-time constant.
+template <int V> struct ActC { static constexpr int value = V; };
+template <class F>
+__device__ __forceinline__ void with_act(int act, F f) {
+  switch (act) {
+    case TERN_ACT_RELU: f(ActC<TERN_ACT_RELU>{}); break;
+    case TERN_ACT_RELU2: f(ActC<TERN_ACT_RELU2>{}); break;
+    case TERN_ACT_SILU: f(ActC<TERN_ACT_SILU>{}); break;
+    case TERN_ACT_GELU: f(ActC<TERN_ACT_GELU>{}); break;
+    case TERN_ACT_GELU_TANH: f(ActC<TERN_ACT_GELU_TANH>{}); break;
+    default: f(ActC<TERN_ACT_NONE>{});
   }
 }
 

@@ -13,8 +13,9 @@
 //     fp16 s t in registers (exact) and store them with tcgen05.st; 32 columns hold 64 terms.
 //   * Tensor memory: two accumulators of up to 192 columns, so that the epilogue of a tile runs beside the
 //     MMAs of the next, and a ring of 4 to 8 A stages of 32 columns in what they leave.
-//   * Warps: 0 and 2 TMA, 1 MMA, 4-7 epilogue, 8 on decode (four sets of four; a set takes every fourth stage,
-//     which hides the latencies between a stage's arrival and its decoded weights').
+//   * Warps: 0 and 2 TMA, 1 MMA, 4-11 epilogue (two for each 32 rows of A, every other 16 columns each), 12 on
+//     decode (three sets of four; a set takes every third stage, which hides the latencies between a stage's
+//     arrival and its decoded weights').
 //   * bn is chosen by the host so that the tiles fill whole waves of CTAs.
 //   * Transposed: A's rows are the columns of the packed rows, whose group is one scale per packed row.
 //     ldmatrix.trans hands a lane 16-bit pieces of two adjacent rows; each field of theirs is a finished
@@ -37,8 +38,10 @@ constexpr int BK = 64;       // terms per stage (one 128-byte swizzle row of fp1
 constexpr int kMaxBN = 192;  // rows of x per tile (of a pair of CTAs)
 constexpr int STAGES = 8;    // TMA ring
 constexpr int ASTAGES = 8;   // A ring in tensor memory, at most: what the accumulators leave of it
-constexpr int SETS = 4;      // sets of four decoder warps; a set takes every SETS-th stage
-constexpr int kThreads = 256 + SETS * 128;
+// 24 warps: the forward epilogue has more to do, the transposed decoding
+constexpr int kThreads = 768, kMaxSets = 4;
+constexpr int epi_warps(bool trans) { return trans ? 4 : 8; }
+constexpr int decoder_sets(bool trans) { return (kThreads / 32 - 4 - epi_warps(trans)) / 4; }
 constexpr uint32_t kTmemCols = 512;  // accumulators at 0 and bn, the A ring from 2 bn on
 constexpr uint64_t kWaitNs = 1000000000ull;
 
@@ -46,7 +49,7 @@ constexpr int X_BYTES = kMaxBN / 2 * BK * 2;  // a CTA's half of the tile's rows
 constexpr int P_BYTES = BM * 32;  // codes of a stage: forward 128 rows x 16 or 32 bytes, transposed 64 x 16, 32 or 48
 constexpr int OFF_P = STAGES * X_BYTES;
 constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;  // transposed base-3: two tiles of each set in Q2's form [64][32]
-constexpr int OFF_LUT = OFF_Q + 2 * SETS * 64 * 32;
+constexpr int OFF_LUT = OFF_Q + 2 * kMaxSets * 64 * 32;
 constexpr int OFF_BAR = OFF_LUT + 256 * 32 * 4;
 constexpr int NUM_BARS = 2 * STAGES + 2 * ASTAGES + 4 + 1;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
@@ -217,12 +220,69 @@ __device__ __forceinline__ void t3_words(int v5, const uint8_t* p, const uint32_
   }
 }
 
+// ---- epilogue --------------------------------------------------------------------------------------------
+// 16 rows of x from t0 on of output j: this lane writes the first `lim`. r arrives from tensor memory.
+template <int ACT>
+__device__ __forceinline__ void finish(const Params& p, uint32_t (&r)[16], float bias, int64_t t0, int64_t j, int lim) {
+  uint16_t rv[16];
+  if (p.e.residual) {
+    const uint16_t* res = p.e.residual + t0 * p.nout + j;
+#pragma unroll
+    for (int i = 0; i < 16; i++, res += p.nout)
+      if (i < lim) rv[i] = *res;
+  }
+  tmem_ld_wait();
+  if (p.e.preact) {
+    uint16_t* z = p.e.preact + t0 * p.n + j;
+#pragma unroll
+    for (int i = 0; i < 16; i++, z += p.n)
+      if (i < lim) *z = f2h(__uint_as_float(r[i]) + bias);
+  }
+  uint16_t* y = p.y + t0 * p.nout + j;
+#pragma unroll
+  for (int i = 0; i < 16; i++, y += p.nout) {
+    float v = act_fwd(ACT, __uint_as_float(r[i]) + bias);
+    if (p.e.residual) v += h2f(rv[i]);
+    if (i < lim) *y = f2h(v);
+  }
+}
+// Lanes l and l + 16 hold the gate and the up sums of one output; of two rows of x the lower lane finishes
+// the first, the upper one (`up`) the second.
+template <int ACT>
+__device__ __forceinline__ void finish_gated(const Params& p, uint32_t (&r)[16], float bias, int64_t t0, int64_t j, int lim, bool up) {
+  const int own = up ? 1 : 0;
+  uint16_t rv[8];
+  if (p.e.residual) {
+    const uint16_t* res = p.e.residual + (t0 + own) * p.nout + j;
+#pragma unroll
+    for (int i = 0; i < 8; i++, res += 2 * p.nout)
+      if (2 * i + own < lim) rv[i] = *res;
+  }
+  tmem_ld_wait();
+  if (p.e.preact) {
+    uint16_t* z = p.e.preact + t0 * p.n + j + (up ? p.nout : 0);
+#pragma unroll
+    for (int i = 0; i < 16; i++, z += p.n)
+      if (i < lim) *z = f2h(__uint_as_float(r[i]) + bias);
+  }
+  uint16_t* y = p.y + (t0 + own) * p.nout + j;
+#pragma unroll
+  for (int i = 0; i < 8; i++, y += 2 * p.nout) {
+    const float z0 = __uint_as_float(r[2 * i]) + bias, z1 = __uint_as_float(r[2 * i + 1]) + bias;
+    const float got = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
+    float v = act_fwd(ACT, up ? got : z0) * (up ? z1 : got);
+    if (p.e.residual) v += h2f(rv[i]);
+    if (2 * i + own < lim) *y = f2h(v);
+  }
+}
+
 // ---- the kernel ------------------------------------------------------------------------------------------
 template <int LAYOUT, bool TRANS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  constexpr int kEpi = epi_warps(TRANS), SETS = decoder_sets(TRANS), kFirstDecoder = 4 + kEpi;
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + OFF_BAR);  // TMA -> decoders, MMA
   uint64_t* empty = full + STAGES;                               // MMA -> TMA
   uint64_t* dfull = empty + STAGES;                              // decoders -> MMA
@@ -245,7 +305,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; i++) { mbar_init(full + i, 2); mbar_init(empty + i, 1); }
     for (int i = 0; i < ASTAGES; i++) { mbar_init(dfull + i, 8); mbar_init(dempty + i, 1); }
-    for (int i = 0; i < 2; i++) { mbar_init(tfull + i, 1); mbar_init(tempty + i, 8); }
+    for (int i = 0; i < 2; i++) { mbar_init(tfull + i, 1); mbar_init(tempty + i, 2 * kEpi); }
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -363,7 +423,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       }
     }
     __syncwarp();
-  } else if (warp >= 4 && warp < 8) {
+  } else if (warp >= 4 && warp < kFirstDecoder) {
     // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3;
     // the A row of this lane is output `o` of the tile (of the gate, or with `up` of the up projection)
@@ -384,57 +444,31 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       const uint32_t taddr = tmem + acc * p.bn + ((uint32_t)(quad * 32) << 16);
       const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);  // rows of x in this tile
 #pragma unroll 1
-      for (int c0 = 0; c0 < cols; c0 += 16) {
+      for (int c0 = 4 * (warp & ~3) - 16; c0 < cols; c0 += 4 * kEpi) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(taddr + c0, r);
-        uint16_t* y = p.y + (m0 + c0) * p.nout + j;
-        const uint16_t* res = !TRANS && p.e.residual ? p.e.residual + (m0 + c0) * p.nout + j : nullptr;
-        uint16_t rv[16];
-        if (!TRANS && res && !gated) {
+        const int lim = in ? cols - c0 : 0;  // rows of x that this lane writes
+        const int64_t t0 = m0 + c0;
+        if constexpr (TRANS) {
+          tmem_ld_wait();
+          uint16_t* y = p.y + t0 * p.nout + j;
 #pragma unroll
-          for (int i = 0; i < 16; i++) rv[i] = in && c0 + i < cols ? res[i * p.nout] : (uint16_t)0;
-        }
-        tmem_ld_wait();
-        if (TRANS || !gated) {
-#pragma unroll
-          for (int i = 0; i < 16; i++) {
-            if (!in || c0 + i >= cols) continue;
-            float v = __uint_as_float(r[i]);
-            if (!TRANS) {
-              v += bias;
-              if (p.e.preact) p.e.preact[(m0 + c0 + i) * p.n + j] = f2h(v);
-              v = act_fwd(p.e.act, v);
-              if (res) v += h2f(rv[i]);
-            }
-            y[i * p.nout] = f2h(v);
-          }
+          for (int i = 0; i < 16; i++, y += p.nout)
+            if (i < lim) *y = f2h(__uint_as_float(r[i]));
         } else {
-          // lanes l and l + 16 hold the gate and the up sum of one output; of two rows of x the lower lane
-          // finishes the first, the upper one the second
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float z0 = __uint_as_float(r[i]) + bias, z1 = __uint_as_float(r[i + 1]) + bias;
-            const float got = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
-            const int t = i + (up ? 1 : 0);
-            if (p.e.preact && in) {
-              uint16_t* z = p.e.preact + (m0 + c0 + i) * p.n + j + (up ? p.nout : 0);
-              if (c0 + i < cols) z[0] = f2h(z0);
-              if (c0 + i + 1 < cols) z[p.n] = f2h(z1);
-            }
-            if (!in || c0 + t >= cols) continue;
-            float v = act_fwd(p.e.act, up ? got : z0) * (up ? z1 : got);
-            if (res) v += h2f(res[t * p.nout]);
-            y[t * p.nout] = f2h(v);
-          }
+          with_act(p.e.act, [&](auto act) {
+            if (gated) finish_gated<act.value>(p, r, bias, t0, j, lim, up);
+            else finish<act.value>(p, r, bias, t0, j, lim);
+          });
         }
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_first(tempty + acc);
     }
-  } else if (warp >= 8) {
+  } else if (warp >= kFirstDecoder) {
     // ------------------------------------------------------------------ decoders
-    const int quad = warp & 3, set = (warp - 8) >> 2, st = threadIdx.x & 127;
+    const int quad = warp & 3, set = (warp - kFirstDecoder) >> 2, st = threadIdx.x & 127;
     const uint32_t a_lane = tmem + a_col + ((uint32_t)(quad * 32) << 16);
     // stage and A slot of the set's next block, with the parities to wait for
     int s = set % STAGES, d = set % (int)a_stages, kb = set, flip = 0;

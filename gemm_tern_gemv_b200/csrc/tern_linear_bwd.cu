@@ -1,7 +1,7 @@
 // Backward of the fused linear layer: dz = dy * act'(z), dbias = sum over rows of dz, dx = dz W.
 //
 // dz and dbias come from one pass (dz_kernel), bound by HBM: dy and z are read once, dz is written once.
-// A CTA takes 32 x VEC columns and a slice of the rows, a warp every eighth of them, a lane VEC columns
+// A CTA takes 16 x VEC columns and a slice of the rows, a half-warp every sixteenth of them, a lane VEC columns
 // (16 bytes where rows are aligned to that). Column sums stay in fp32 registers, are joined over the warps
 // through shared memory and over the row slices through the cluster's shared memory, always in the same
 // order. dx is the transposed product of tern_layer_gemm.cu on the rounded dz.
@@ -10,7 +10,7 @@
 namespace tern {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 8, kLanes = 16, kRowsAtOnce = kWarps * 32 / kLanes;
 
 struct DzParams {
   const uint16_t *dy, *z;
@@ -55,52 +55,51 @@ __device__ __forceinline__ float ld_peer(const float* local, uint32_t rank) {
 }
 
 template <int VEC>
-__global__ void __launch_bounds__(kWarps * 32) dz_kernel(const __grid_constant__ DzParams p) {
-  constexpr int kCols = 32 * VEC;
-  __shared__ float sums[2][kWarps][kCols];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ void dz_rows(const DzParams& p, int act, int64_t c, int64_t t0, int64_t t1, float (&s0)[VEC], float (&s1)[VEC]) {
+#pragma unroll 2
+  for (int64_t t = t0; t < t1; t += kRowsAtOnce) {
+    const Halves<VEC> d = load_halves<VEC>(p.dy + t * p.nout + c);
+    Halves<VEC> a{}, u{}, o0, o1;
+    if (!p.identity) a = load_halves<VEC>(p.z + t * p.n + c);
+    if (p.gated) u = load_halves<VEC>(p.z + t * p.n + p.nout + c);
+#pragma unroll
+    for (int i = 0; i < VEC; i++) {
+      const float g = h2f(d.v[i]), za = h2f(a.v[i]);
+      float f, df;
+      act_both(act, za, &f, &df);
+      const float x0 = (p.gated ? g * h2f(u.v[i]) : g) * df, x1 = g * f;
+      s0[i] += x0;
+      s1[i] += x1;
+      o0.v[i] = f2h(x0);
+      o1.v[i] = f2h(x1);
+    }
+    if (p.dz) {
+      store_halves<VEC>(p.dz + t * p.dz_stride + c, o0);
+      if (p.gated) store_halves<VEC>(p.dz + t * p.dz_stride + p.nout + c, o1);
+    }
+  }
+}
+
+template <int VEC>
+__global__ void __launch_bounds__(kWarps * 32, 3) dz_kernel(const __grid_constant__ DzParams p) {
+  constexpr int kCols = kLanes * VEC;
+  __shared__ float sums[2][kRowsAtOnce][kCols];
+  const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int64_t c = (int64_t)blockIdx.x * kCols + lane * VEC;
   const int64_t r0 = p.m * blockIdx.y / gridDim.y, r1 = p.m * (blockIdx.y + 1) / gridDim.y;
   float s0[VEC] = {}, s1[VEC] = {};
-  if (c < p.nout) {
-    for (int64_t t = r0 + warp; t < r1; t += kWarps) {
-      const Halves<VEC> d = load_halves<VEC>(p.dy + t * p.nout + c);
-      Halves<VEC> a{}, u{}, o0, o1;
-      if (!p.identity) a = load_halves<VEC>(p.z + t * p.n + c);
-      if (p.gated) u = load_halves<VEC>(p.z + t * p.n + p.nout + c);
-#pragma unroll
-      for (int i = 0; i < VEC; i++) {
-        const float g = h2f(d.v[i]), za = h2f(a.v[i]);
-        if (p.gated) {
-          float f, df;
-          act_both(p.act, za, &f, &df);
-          const float x0 = g * h2f(u.v[i]) * df, x1 = g * f;
-          s0[i] += x0;
-          s1[i] += x1;
-          o0.v[i] = f2h(x0);
-          o1.v[i] = f2h(x1);
-        } else {
-          const float x0 = p.identity ? g : g * act_bwd(p.act, za);
-          s0[i] += x0;
-          o0.v[i] = f2h(x0);
-        }
-      }
-      if (p.dz) {
-        store_halves<VEC>(p.dz + t * p.dz_stride + c, o0);
-        if (p.gated) store_halves<VEC>(p.dz + t * p.dz_stride + p.nout + c, o1);
-      }
-    }
-  }
+  if (c < p.nout)
+    with_act(p.act, [&](auto act) { dz_rows<VEC>(p, act.value, c, r0 + sub, r1, s0, s1); });
   if (!p.db) return;  // the same for every CTA of the cluster
 #pragma unroll
   for (int i = 0; i < VEC; i++) {
-    sums[0][warp][lane * VEC + i] = s0[i];
-    sums[1][warp][lane * VEC + i] = s1[i];
+    sums[0][sub][lane * VEC + i] = s0[i];
+    sums[1][sub][lane * VEC + i] = s1[i];
   }
   __syncthreads();
   for (int i = threadIdx.x; i < 2 * kCols; i += kWarps * 32) {
     float s = 0.f;
-    for (int w = 0; w < kWarps; w++) s += sums[i / kCols][w][i % kCols];
+    for (int w = 0; w < kRowsAtOnce; w++) s += sums[i / kCols][w][i % kCols];
     sums[i / kCols][0][i % kCols] = s;  // only this thread reads and writes column i's sums
   }
   cluster_sync_all();
@@ -117,7 +116,7 @@ __global__ void __launch_bounds__(kWarps * 32) dz_kernel(const __grid_constant__
 
 template <int VEC>
 cudaError_t launch_dz(const DzParams& p, cudaStream_t st) {
-  const int64_t cols = 32 * VEC;
+  const int64_t cols = kLanes * VEC;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((p.nout + cols - 1) / cols), p.m >= 64 ? 8 : p.m >= 16 ? 2 : 1);
   cfg.blockDim = dim3(kWarps * 32);
