@@ -10,7 +10,7 @@
 //     shared memory gives, and would cross from L2 at 64 bytes a cycle and SM, more than L2 gives (a version
 //     of this kernel without pairs stopped at 0.9 PFLOP/s there). As a pair each CTA brings half of B. And
 //     A does not go through shared memory at all, it lives in tensor memory: decoder warps turn codes into
-//     fp16 s t in registers (exact) and store them with tcgen05.st; 32 columns hold 64 terms.
+//     fp16 2 s t (binary: s t) in registers, exactly, and store them with tcgen05.st; 32 columns hold 64 terms.
 //   * Tensor memory: two accumulators of up to 192 columns, so that the epilogue of a tile runs beside the
 //     MMAs of the next, and a ring of 4 to 8 A stages of 32 columns in what they leave.
 //   * Warps: 0 and 2 TMA, 1 MMA, 4-11 epilogue (two for each 32 rows of A, every other 16 columns each), 12 on
@@ -40,6 +40,7 @@ constexpr int STAGES = 8;    // TMA ring
 constexpr int ASTAGES = 8;   // A ring in tensor memory, at most: what the accumulators leave of it
 // 24 warps: the forward epilogue has more to do, the transposed decoding
 constexpr int kThreads = 768, kMaxSets = 4;
+constexpr int kEpiBarrier = 1, kSetBarrier = 2;  // named barriers: the epilogue's, and one for each decoder set
 constexpr int epi_warps(bool trans) { return trans ? 4 : 8; }
 constexpr int decoder_sets(bool trans) { return (kThreads / 32 - 4 - epi_warps(trans)) / 4; }
 constexpr uint32_t kTmemCols = 512;  // accumulators at 0 and bn, the A ring from 2 bn on
@@ -50,7 +51,9 @@ constexpr int P_BYTES = BM * 32;  // codes of a stage: forward 128 rows x 16 or 
 constexpr int OFF_P = STAGES * X_BYTES;
 constexpr int OFF_Q = OFF_P + STAGES * P_BYTES;  // transposed base-3: two tiles of each set in Q2's form [64][32]
 constexpr int OFF_LUT = OFF_Q + 2 * kMaxSets * 64 * 32;
-constexpr int OFF_BAR = OFF_LUT + 256 * 32 * 4;
+constexpr int kBigTiles = 16;  // tiles that decoders may be ahead of the epilogue, and more
+constexpr int OFF_BIG = OFF_LUT + 256 * 32 * 4;
+constexpr int OFF_BAR = OFF_BIG + kBigTiles * BM;
 constexpr int NUM_BARS = 2 * STAGES + 2 * ASTAGES + 4 + 1;
 constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
 constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;  // + slack to align the base to 1024
@@ -62,6 +65,10 @@ struct Params {
   int64_t nout;          // outputs of a row: n, n / 2 (gated) or k (transposed)
   int terms;             // length of the sum: k or n
   int bn, rtiles, mtiles;
+  const uint16_t* x;
+  int64_t xstride;
+  const uint8_t* codes;
+  int64_t cstride;
   const uint16_t* scales;
   int64_t sstride;
   uint16_t* y;
@@ -171,22 +178,41 @@ __device__ __forceinline__ bool bar_all(int id, int threads, bool fine) {
 }
 
 // ---- decoding ------------------------------------------------------------------------------------------
-// fp16 pair s t from the pair's fp16 values 2 t: halved first, so that no scale can overflow.
-__device__ __forceinline__ uint32_t scaled(uint32_t two_t, __half2 s2) {
-  const __half2 v = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&two_t), __half2half2(__ushort_as_half(0x3800))), s2);
+// Scales from 2^15 on (kBigScale, as fp16 bits): 2 s does not fit fp16. The outputs they belong to are
+// computed term by term in the epilogue instead.
+constexpr uint32_t kBigScale = 0x7800;
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
-// Codes 2j and 2j + 1 of a word (16 two's-complement fields): one multiply brings them to bits 14..15 and
-// 30..31, where a field is the sign and top exponent bit of +-2.0 (or 0).
-__device__ __forceinline__ uint32_t pair_q2(uint32_t w, int j) {
-  const int jj = j & 3, a = 14 - 4 * jj;
-  const uint32_t x = (j < 4 ? w : w >> 16) & (0xFu << (4 * jj));
-  return (x * ((1u << a) + (1u << (a + 14)))) & 0xC000C000u;
+// 16 two's-complement fields of a word -> eight fp16 pairs 2 s t (s2: s in both halves). A field in the top
+// bits of a half's high byte is +-2.0 or 0: shifted copies of the word hold field f of every byte there, one
+// permute takes the bytes of two adjacent weights from two of them, one mask leaves the fields.
+__device__ __forceinline__ void pairs_q2(uint32_t w, uint32_t s2, uint32_t* o) {
+  const uint32_t v[4] = {w << 6, w << 4, w << 2, w};  // field f of every byte at its top
+#pragma unroll
+  for (int j = 0; j < 8; j++)  // weights 2j and 2j + 1: fields f, f + 1 of byte j / 2
+    o[j] = hmul2(__byte_perm(v[2 * (j & 1)], v[2 * (j & 1) + 1], (j >> 1) << 4 | (4 + (j >> 1)) << 12) & 0xC000C000u, s2);
 }
-// Sign bits p and p + 1 (p even, <= 14): +-1.0 (0x3C00 / 0xBC00).
-__device__ __forceinline__ uint32_t pair_q1(uint32_t w, int p) {
-  const uint32_t x = w & (3u << p);
-  return ((x * ((1u << (15 - p)) + (1u << (30 - p)))) & 0x80008000u) ^ 0xBC00BC00u;
+// The same with a multiplication for the permute and the shifts, where base-3's table needs the ALU: it brings
+// the two fields of a pair, masked first, to bits 14..15 and 30..31.
+__device__ __forceinline__ void pairs_mul(uint32_t w, uint32_t s2, uint32_t* o) {
+#pragma unroll
+  for (int j = 0; j < 8; j++) {
+    const int jj = j & 3, a = 14 - 4 * jj;
+    const uint32_t x = (j < 4 ? w : w >> 16) & (0xFu << (4 * jj));
+    o[j] = hmul2((x * ((1u << a) + (1u << (a + 14)))) & 0xC000C000u, s2);
+  }
+}
+// 32 sign bits -> sixteen fp16 pairs s t: the bit of a weight at the top of a half, flipped into the sign of s.
+__device__ __forceinline__ void pairs_q1(uint32_t w, uint32_t s2, uint32_t* o) {
+  uint32_t v[8];  // bit f of every byte at its top
+#pragma unroll
+  for (int f = 0; f < 8; f++) v[f] = w << (7 - f);
+#pragma unroll
+  for (int j = 0; j < 16; j++)
+    o[j] = (~__byte_perm(v[2 * (j & 3)], v[2 * (j & 3) + 1], (j >> 2) << 4 | (4 + (j >> 2)) << 12) & 0x80008000u) ^ s2;
 }
 // 64 trits as four words of 16 two's-complement fields. Trit 64 q starts at digit (64 q) mod 5 of byte
 // (64 q) / 5, which is 0, 12, 9, 6 or 3 past a 16-byte boundary for q mod 5 = V = 0 .. 4: u and v are the 32
@@ -220,10 +246,23 @@ __device__ __forceinline__ void t3_words(int v5, const uint8_t* p, const uint32_
   }
 }
 
+// A sum whose weights' scales 2 s t cannot hold, term by term: row t of x and output (packed row, transposed:
+// column) `o`, in the accumulators' unit.
+template <int LAYOUT, bool TRANS>
+__device__ __noinline__ float term_by_term(const uint16_t* x, const uint8_t* codes, int64_t cstride, const uint16_t* scales,
+                                           int64_t sstride, int terms, int64_t o) {
+  float z = 0.f;
+  for (int64_t q = 0; q < terms; q++) {
+    const int64_t n = TRANS ? q : o, k = TRANS ? o : q;
+    z = fmaf(h2f(scales[n * sstride + k / kGroup]) * decode_t(LAYOUT, codes + n * cstride, k), h2f(x[q]), z);
+  }
+  return 2.f * z;
+}
+
 // ---- epilogue --------------------------------------------------------------------------------------------
 // 16 rows of x from t0 on of output j: this lane writes the first `lim`. r arrives from tensor memory.
 template <int ACT>
-__device__ __forceinline__ void finish(const Params& p, uint32_t (&r)[16], float bias, int64_t t0, int64_t j, int lim) {
+__device__ __forceinline__ void finish(const Params& p, uint32_t (&r)[16], float half, float bias, int64_t t0, int64_t j, int lim) {
   uint16_t rv[16];
   if (p.e.residual) {
     const uint16_t* res = p.e.residual + t0 * p.nout + j;
@@ -231,17 +270,16 @@ __device__ __forceinline__ void finish(const Params& p, uint32_t (&r)[16], float
     for (int i = 0; i < 16; i++, res += p.nout)
       if (i < lim) rv[i] = *res;
   }
-  tmem_ld_wait();
   if (p.e.preact) {
     uint16_t* z = p.e.preact + t0 * p.n + j;
 #pragma unroll
     for (int i = 0; i < 16; i++, z += p.n)
-      if (i < lim) *z = f2h(__uint_as_float(r[i]) + bias);
+      if (i < lim) *z = f2h(fmaf(__uint_as_float(r[i]), half, bias));
   }
   uint16_t* y = p.y + t0 * p.nout + j;
 #pragma unroll
   for (int i = 0; i < 16; i++, y += p.nout) {
-    float v = act_fwd(ACT, __uint_as_float(r[i]) + bias);
+    float v = act_fwd(ACT, fmaf(__uint_as_float(r[i]), half, bias));
     if (p.e.residual) v += h2f(rv[i]);
     if (i < lim) *y = f2h(v);
   }
@@ -249,7 +287,7 @@ __device__ __forceinline__ void finish(const Params& p, uint32_t (&r)[16], float
 // Lanes l and l + 16 hold the gate and the up sums of one output; of two rows of x the lower lane finishes
 // the first, the upper one (`up`) the second.
 template <int ACT>
-__device__ __forceinline__ void finish_gated(const Params& p, uint32_t (&r)[16], float bias, int64_t t0, int64_t j, int lim, bool up) {
+__device__ __forceinline__ void finish_gated(const Params& p, uint32_t (&r)[16], float half, float bias, int64_t t0, int64_t j, int lim, bool up) {
   const int own = up ? 1 : 0;
   uint16_t rv[8];
   if (p.e.residual) {
@@ -258,17 +296,16 @@ __device__ __forceinline__ void finish_gated(const Params& p, uint32_t (&r)[16],
     for (int i = 0; i < 8; i++, res += 2 * p.nout)
       if (2 * i + own < lim) rv[i] = *res;
   }
-  tmem_ld_wait();
   if (p.e.preact) {
     uint16_t* z = p.e.preact + t0 * p.n + j + (up ? p.nout : 0);
 #pragma unroll
     for (int i = 0; i < 16; i++, z += p.n)
-      if (i < lim) *z = f2h(__uint_as_float(r[i]) + bias);
+      if (i < lim) *z = f2h(fmaf(__uint_as_float(r[i]), half, bias));
   }
   uint16_t* y = p.y + (t0 + own) * p.nout + j;
 #pragma unroll
   for (int i = 0; i < 8; i++, y += 2 * p.nout) {
-    const float z0 = __uint_as_float(r[2 * i]) + bias, z1 = __uint_as_float(r[2 * i + 1]) + bias;
+    const float z0 = fmaf(__uint_as_float(r[2 * i]), half, bias), z1 = fmaf(__uint_as_float(r[2 * i + 1]), half, bias);
     const float got = __shfl_xor_sync(0xffffffffu, up ? z0 : z1, 16);
     float v = act_fwd(ACT, up ? got : z0) * (up ? z1 : got);
     if (p.e.residual) v += h2f(rv[i]);
@@ -293,6 +330,8 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   uint32_t* lut = reinterpret_cast<uint32_t*>(smem + OFF_LUT);
+  // per tile (in turn) and row of A: a scale of kBigScale or more was met (transposed: row 0 for the whole tile)
+  volatile uint8_t* big = smem + OFF_BIG;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int rank = (int)cluster_rank(), pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
@@ -310,6 +349,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     *abort_flag = 0;
     fence_mbar_init();
   }
+  for (int i = threadIdx.x; i < kBigTiles * BM; i += kThreads) big[i] = 0;
   if (warp == 0 && lane == 0) { prefetch_tmap(&tmap_x); prefetch_tmap(&tmap_w); }
   if (LAYOUT == TERN_T3_5PB_G128) {
     for (int i = threadIdx.x; i < 256 * 32; i += kThreads) {
@@ -432,6 +472,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     if (!TRANS) o = gated ? quad * 16 + (lane & 15) : quad * 32 + lane;
     else if (LAYOUT == TERN_Q1_0_G128) o = 16 * (lane & 7) + 4 * quad + (lane >> 3);
     else o = 64 * (quad >> 1) + 8 * (lane & 7) + 4 * (quad & 1) + (lane >> 3);
+    constexpr float half = LAYOUT == TERN_Q1_0_G128 ? 1.f : 0.5f;  // the accumulators hold 2 s t x (binary: s t x)
     uint32_t lt = 0;
     for (int tile = pair; tile < tiles; tile += pairs, lt++) {
       const int64_t j = (int64_t)(tile / p.mtiles * 2 + rank) * step + o;  // output column
@@ -439,7 +480,12 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       const bool in = j < p.nout;
       const float bias = !TRANS && p.e.bias && in ? h2f(p.e.bias[j + (up ? p.nout : 0)]) : 0.f;
       const uint32_t acc = lt & 1u;
-      if (!__all_sync(0xffffffffu, mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs))) break;
+      // the warps leave together, and have all read the tile's flags before any of them is cleared
+      const bool fine = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+      volatile uint8_t* flag = big + (lt % kBigTiles) * BM + (TRANS ? 0 : quad * 32 + lane);
+      const bool again = LAYOUT != TERN_Q1_0_G128 && fine && *flag;
+      if (!bar_all(kEpiBarrier, kEpi * 32, fine)) break;
+      if (again) *flag = 0;
       tc_fence_after();
       const uint32_t taddr = tmem + acc * p.bn + ((uint32_t)(quad * 32) << 16);
       const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);  // rows of x in this tile
@@ -449,16 +495,23 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         tmem_ld_32x32b_x16(taddr + c0, r);
         const int lim = in ? cols - c0 : 0;  // rows of x that this lane writes
         const int64_t t0 = m0 + c0;
+        tmem_ld_wait();
+        if (again) {
+#pragma unroll
+          for (int i = 0; i < 16; i++)
+            if (i < lim)
+              r[i] = __float_as_uint(term_by_term<LAYOUT, TRANS>(p.x + (t0 + i) * p.xstride, p.codes, p.cstride, p.scales, p.sstride,
+                                                                 p.terms, j + (up ? p.nout : 0)));
+        }
         if constexpr (TRANS) {
-          tmem_ld_wait();
           uint16_t* y = p.y + t0 * p.nout + j;
 #pragma unroll
           for (int i = 0; i < 16; i++, y += p.nout)
-            if (i < lim) *y = f2h(__uint_as_float(r[i]));
+            if (i < lim) *y = f2h(__uint_as_float(r[i]) * half);
         } else {
           with_act(p.e.act, [&](auto act) {
-            if (gated) finish_gated<act.value>(p, r, bias, t0, j, lim, up);
-            else finish<act.value>(p, r, bias, t0, j, lim);
+            if (gated) finish_gated<act.value>(p, r, half, bias, t0, j, lim, up);
+            else finish<act.value>(p, r, half, bias, t0, j, lim);
           });
         }
       }
@@ -473,8 +526,9 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     // stage and A slot of the set's next block, with the parities to wait for
     int s = set % STAGES, d = set % (int)a_stages, kb = set, flip = 0;
     uint32_t fph = 0, eph = 1;
+    uint32_t lt = 0;
     bool ok = true;
-    for (int tile = pair; tile < tiles && ok; tile += pairs) {
+    for (int tile = pair; tile < tiles && ok; tile += pairs, lt++) {
       const int r0 = (tile / p.mtiles * 2 + rank) * step;
       // forward: this lane's row of A is packed row `row`, at row `src` of the stage's codes
       const int src = gated ? (lane >> 4) * 64 + quad * 16 + (lane & 15) : quad * 32 + lane;
@@ -503,16 +557,13 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
             break;
           }
           tc_fence_after();
-          const __half2 s2 = __half2half2(__ushort_as_half((uint16_t)cur));
+          if ((cur & 0x7fff) >= kBigScale && LAYOUT != TERN_Q1_0_G128) big[(lt % kBigTiles) * BM + quad * 32 + lane] = 1;
+          const uint32_t s2 = cur | cur << 16;
           uint32_t o[32];
-          if (LAYOUT == TERN_Q1_0_G128) {
+          if constexpr (LAYOUT == TERN_Q1_0_G128) {
             const uint2 w = *reinterpret_cast<const uint2*>(P + src * 16 + 8 * (kb & 1));
-#pragma unroll
-            for (int j = 0; j < 32; j++) {
-              const uint32_t one = pair_q1((j < 16 ? w.x : w.y) >> (j & 8 ? 16 : 0), 2 * (j & 7));
-              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&one), s2);
-              o[j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
+            pairs_q1(w.x, s2, o);
+            pairs_q1(w.y, s2, o + 16);
           } else {
             uint32_t w[4];
             if (LAYOUT == TERN_Q2_0_G128) {
@@ -522,7 +573,10 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
               t3_words(kb % 5, P + src * 32, lut + lane, w);
             }
 #pragma unroll
-            for (int j = 0; j < 32; j++) o[j] = scaled(pair_q2(w[j >> 3], j & 7), s2);
+            for (int j = 0; j < 4; j++) {
+              if (LAYOUT == TERN_Q2_0_G128) pairs_q2(w[j], s2, o + 8 * j);
+              else pairs_mul(w[j], s2, o + 8 * j);
+            }
           }
           tmem_st_32x32b_x32(a_lane + d * 32, o);
         } else {
@@ -537,12 +591,13 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
               *reinterpret_cast<uint4*>(smem + OFF_Q + (set * 2 + flip) * 64 * 32 + (st & 63) * 32 + (st & 64 ? 16 : 0)) =
                   make_uint4(w[0], w[1], w[2], w[3]);
             }
-            fine = bar_all(1 + set, 128, fine);  // the four warps leave together
+            fine = bar_all(kSetBarrier + set, 128, fine);  // the four warps leave together
           }
           if (!__all_sync(0xffffffffu, fine)) {
             ok = false;
             break;
           }
+          if (LAYOUT != TERN_Q1_0_G128 && ((cur & 0x7fff) >= kBigScale || ((cur >> 16) & 0x7fff) >= kBigScale)) big[(lt % kBigTiles) * BM] = 1;
           tc_fence_after();
           // columns of 16 bits of the codes: Q2 eight fields (two column groups of 16 bytes), binary 16 bits
           const int group = LAYOUT == TERN_Q1_0_G128 ? 0 : quad >> 1;
@@ -568,15 +623,12 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
 #pragma unroll
               for (int b = 0; b < 2; b++) {
                 const int f = 2 * half + b;  // field f0 + f of both halves of R[q]
-                const __half2 s2 = *reinterpret_cast<const __half2*>(&sp[q]);
                 if (LAYOUT == TERN_Q1_0_G128) {
                   const uint32_t x = R[q] & (0x00010001u << f0 << f);  // bit f0 + f -> bit 15
-                  const uint32_t one = (x * (up_mul << (3 - f))) ^ 0xBC00BC00u;
-                  const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&one), s2);
-                  o[2 * q + b] = *reinterpret_cast<const uint32_t*>(&v);
+                  o[2 * q + b] = (~(x * (up_mul << (3 - f))) & 0x80008000u) ^ sp[q];
                 } else {
                   const uint32_t x = R[q] & (0x00030003u << (2 * f0) << (2 * f));  // field -> bits 14..15
-                  o[2 * q + b] = scaled(x * (up_mul << (6 - 2 * f)), s2);
+                  o[2 * q + b] = hmul2(x * (up_mul << (6 - 2 * f)), sp[q]);
                 }
               }
             }
@@ -611,6 +663,8 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
 template <int LAYOUT, bool TRANS>
 cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, Params& p, cudaStream_t st) {
   CUtensorMap mx, mw;
+  p.x = x;
+  p.xstride = xstride;
   if (!tmap_2d_new(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)p.terms, (uint64_t)p.m, (uint64_t)xstride * 2, BK,
                    (uint32_t)p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
@@ -630,15 +684,16 @@ cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, P
 }
 
 // Rows of x per tile: the multiple of 32 up to kMaxBN that makes the waves of tiles cheapest. 64 terms of a
-// tile cost four MMAs of bn / 2 + 11 cycles (measured), and no less than their decoding (about 290).
+// tile cost four MMAs of bn / 2 + 11 cycles, and no less than what the warps of an SM need to decode them and
+// to finish the tile before (about 480 cycles, measured at bn = 128 and 160).
 int pick_bn(int64_t m, int64_t rtiles, int sms) {
   int best = kMaxBN;
   double cost = -1;
   for (int bn = 32; bn <= kMaxBN; bn += 32) {
     if (bn > 32 && bn - 32 >= m) break;
     const int64_t tiles = (rtiles + 1) / 2 * ((m + bn - 1) / bn), waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const double c = (double)waves * std::max(2 * bn + 44, 290);
-    if (cost < 0 || c <= cost) {
+    const double c = (double)waves * std::max(2 * bn + 44, 480);
+    if (cost < 0 || c < cost) {
       cost = c;
       best = bn;
     }
@@ -660,6 +715,8 @@ Params common(const tern_matrix& W, int64_t m, uint32_t* status) {
   p.m = m;
   p.n = W.n;
   p.k = W.k;
+  p.codes = static_cast<const uint8_t*>(W.codes);
+  p.cstride = W.code_row_stride;
   p.scales = W.scales;
   p.sstride = W.scale_row_stride;
   p.status = status;

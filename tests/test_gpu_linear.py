@@ -264,3 +264,25 @@ def test_refused_operands():
     codes, s, _ = weights(T.Q2_0_G128, 33, 256, 60)
     with pytest.raises(T.TernError):
         T.linear(_matrix(codes, s, T.Q2_0_G128, 256), x, gated=True)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("m", [1, 7, 40, 200])
+@pytest.mark.parametrize("gated", [False, True])
+def test_extreme_scales(layout, m, gated):
+    # scales near fp16's largest value (twice them does not fit) and in its subnormal range, side by side
+    n, k = 300, 384
+    codes, s, w = weights(layout, n, k, 70)
+    t = np.sign(w)
+    s[:] = np.float16(2.0 ** -16)
+    s[5, 1], s[17, 0], s[n // 2 + 5, 2], s[n - 1, 2] = 65504.0, 40000.0, -33000.0, 32768.0
+    s[20, 0], s[21, 1] = np.float16(2.0 ** -24), np.float16(3 * 2.0 ** -24)
+    w = t * np.repeat(s.astype(np.float64), 128, axis=1)
+    x = half(71, m, k, scale=2.0 ** -10)
+    for rows in (slice(0, m),):
+        y = T.linear(_matrix(codes, s, layout, k), _dev(x[rows]), act="relu" if gated else "none", gated=gated).cpu().numpy()
+        args = (w, f64(x[rows]), None, "relu" if gated else "none", gated)
+        want, bound = L.linear(*args), L.linear_bound(*args)
+        fits = np.abs(want) < 65000
+        check(np.where(fits, y, 0), np.where(fits, want, 0), bound, "extreme scales")
+        assert np.isinf(y[~fits]).all() or fits.all()

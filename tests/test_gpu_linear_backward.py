@@ -175,3 +175,17 @@ def test_refused_operands():
             T.linear_backward(W, **{"dy": dy, **bad})
     with pytest.raises(T.TernError):
         T.linear_backward(W, dy[:0])
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("m", [1, 40])
+def test_extreme_scales(layout, m):
+    # scales whose double does not fit fp16, beside subnormal ones
+    n, k = 200, 384
+    codes, s, w = weights(layout, n, k, 70)
+    s[:] = np.float16(2.0 ** -16)
+    s[5, 1], s[150, 1], s[7, 2] = 65504.0, -40000.0, np.float16(2.0 ** -24)
+    w = np.sign(w) * np.repeat(s.astype(np.float64), 128, axis=1)
+    dy = half(71, m, n, scale=2.0 ** -10)
+    dx, _, _ = T.linear_backward(_matrix(codes, s, layout, k), _dev(dy))
+    check(dx.cpu().numpy(), f64(dy) @ w, L.backward_bounds(w, f64(dy), None)[0], "extreme scales")
