@@ -139,14 +139,14 @@ struct MoeParams {
   uint16_t* y;               // [tokens][d]
   float* weights;            // [tokens][top_k]
   int32_t* ids;              // [tokens][top_k]
-  float* h;                  // [tokens * top_k][f] expert activations
-  uint32_t* status;          // device status word or null
+  uint32_t* clear;           // largest |h| of each (token, expert) pair as bits, then a counter per 16 columns of y
+  float *h, *z;              // [tokens * top_k][f] expert activations, [tokens * top_k][d] their down products
   int tokens, d, f, experts, top_k, act, renormalize;
 };
 struct MoePlan {  // workspace offsets
-  size_t ids, weights, h, bytes;
+  size_t ids, weights, clear, h, z, bytes;
 };
-MoePlan moe_plan(int64_t tokens, int64_t d, int64_t f, int experts, int top_k);
+MoePlan moe_plan(int64_t tokens, int64_t d, int64_t f, int top_k);
 cudaError_t launch_moe(const tern_matrix& G, const tern_matrix& D, MoeParams p, const MoePlan& plan, void* workspace,
                        cudaStream_t st);
 
