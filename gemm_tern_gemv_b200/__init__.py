@@ -113,7 +113,7 @@ SIGNATURES = {
     "tern_moe_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(TernMoeLayerC), ctypes.c_int64]),
     "tern_moe": (ctypes.c_int, [ctypes.POINTER(TernMoeLayerC), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
                                 ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
-                                ctypes.c_void_p, ctypes.c_void_p]),
+                                ctypes.c_void_p]),
     "tern_device_result": (ctypes.c_int, [ctypes.c_uint32, ctypes.c_int64]),
     "tern_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "tern_version": (ctypes.c_int32, []),
@@ -430,17 +430,20 @@ def gemm(W: TernMatrix, X, Y=None, status=None):
 
 
 # ------------------------------------------------------------------------------- layer operators
-def _need(t, name, shape, dtype, device, contiguous=True):
-    """Checks an operand of a layer operator: a tensor of this shape and type on `device`."""
-    if tuple(t.shape) != shape or t.dtype != dtype or t.device != device:
+# One call of these costs the host about as long as the GPU takes for a single token, so the checks
+# are written to be cheap.
+def _need(t, name, shape, dtype, device):
+    """Checks an output of a layer operator: a contiguous tensor of this shape and type on `device`."""
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name}: needs {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
-    if contiguous and not t.is_contiguous():
+    if not t.is_contiguous():
         raise ValueError(f"{name}: needs a contiguous tensor")
 
 
 def _operand(t, name, shape, dtype, device):
     """An input of a layer operator: checked, and a contiguous 16-byte aligned copy where it is neither."""
-    _need(t, name, shape, dtype, device, contiguous=False)
+    if t.shape != shape or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name}: needs {dtype} {list(shape)} on {device}, got {t.dtype} {list(t.shape)} on {t.device}")
     if not t.is_contiguous():
         t = t.contiguous()
     return t if t.data_ptr() % 16 == 0 else t.clone()
@@ -453,17 +456,30 @@ def _layer_matrix(W: TernMatrix, name: str, device):
 
 
 def _act_id(act: str) -> int:
-    if act not in ACTS:
+    a = ACTS.get(act)
+    if a is None:
         raise ValueError(f"act: one of {sorted(ACTS)}, got {act!r}")
-    return ACTS[act]
+    return a
 
 
-def _on_device(device):
-    """The context in which to allocate and launch for tensors on `device`, or None when it is current."""
-    torch = _torch()
+def _status_ptr(status, device):
+    if status is None:
+        return None
+    if status.device != device:
+        raise ValueError(f"status: needs a tensor on {device}, got {status.device}")
+    return status.data_ptr()
+
+
+def _is_current(torch, device) -> bool:
+    """Whether `device` is the current CUDA device (the calls below allocate and launch there)."""
     if device.type != "cuda":
         raise ValueError(f"the layer operators run on CUDA tensors, got {device}")
-    return None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+    return device.index == torch.cuda.current_device()
+
+
+def _raw_stream(torch, device) -> int:
+    """The current stream of `device` as an address, without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def linear(W: TernMatrix, x, bias=None, act: str = "none", gated: bool = False, residual=None, y=None, preact=None,
@@ -476,38 +492,39 @@ def linear(W: TernMatrix, x, bias=None, act: str = "none", gated: bool = False, 
     [m][n_out], may be y itself; preact: an fp16 [m][n] tensor that receives z + bias for linear_backward;
     static_weights: no pending GPU work writes W; status: int32 tensor, DEVICE_TIMEOUT is OR-ed in when a pipeline
     wait runs out. Raises ValueError for operands of other shapes, types or devices."""
-    device = x.device
-    other = _on_device(device)
-    if other is not None:
-        with other:
-            return linear(W, x, bias, act, gated, residual, y, preact, static_weights, status)
     torch = _torch()
+    device = x.device
+    if not _is_current(torch, device):
+        with torch.cuda.device(device):
+            return linear(W, x, bias, act, gated, residual, y, preact, static_weights, status)
     half = torch.float16
-    lead = x.shape[:-1]
-    if x.dim() not in (1, 2):
-        raise ValueError(f"x: needs [k] or [m][k], got {list(x.shape)}")
-    m = x.shape[0] if x.dim() == 2 else 1
-    n_out = W.n // 2 if gated else W.n
-    x = _operand(x, "x", (*lead, W.k), half, device)
+    shape = x.shape
+    if len(shape) not in (1, 2):
+        raise ValueError(f"x: needs [k] or [m][k], got {list(shape)}")
+    m = shape[0] if len(shape) == 2 else 1
+    lead = (m,) if len(shape) == 2 else ()
+    out = lead + (W.n // 2 if gated else W.n,)
+    x = _operand(x, "x", lead + (W.k,), half, device)
     c = _layer_matrix(W, "W", device)
-    e = TernEpilogueC(_act_id(act), 1 if gated else 0, None, None, None)
+    if y is None:
+        y = x.new_empty(out)
+    else:
+        _need(y, "y", out, half, device)
+    b = r = z = None
     if bias is not None:
         bias = _operand(bias, "bias", (W.n,), half, device)
-        e.bias = bias.data_ptr()
-    if y is None:
-        y = torch.empty((*lead, n_out), dtype=half, device=device)
-    else:
-        _need(y, "y", (*lead, n_out), half, device)
+        b = bias.data_ptr()
     if residual is not None:
         if residual is not y:
-            residual = _operand(residual, "residual", (*lead, n_out), half, device)
-        e.residual = residual.data_ptr()
+            residual = _operand(residual, "residual", out, half, device)
+        r = residual.data_ptr()
     if preact is not None:
-        _need(preact, "preact", (*lead, W.n), half, device)
-        e.preact = preact.data_ptr()
-    st = lib().tern_linear(c, x.data_ptr(), m, y.data_ptr(), e, GEMV_STATIC_WEIGHTS if static_weights else 0,
-                           status.data_ptr() if status is not None else None, torch.cuda.current_stream().cuda_stream)
-    _check(st, "tern_linear")
+        _need(preact, "preact", lead + (W.n,), half, device)
+        z = preact.data_ptr()
+    st = lib().tern_linear(c, x.data_ptr(), m, y.data_ptr(), TernEpilogueC(_act_id(act), 1 if gated else 0, b, r, z),
+                           GEMV_STATIC_WEIGHTS if static_weights else 0, _status_ptr(status, device), _raw_stream(torch, device))
+    if st:
+        _check(st, "tern_linear")
     return y
 
 
@@ -517,39 +534,37 @@ def linear_backward(W: TernMatrix, dy, preact=None, act: str = "none", gated: bo
     (tern_linear_backward); dx / dbias are None when not needed. dz is the gradient of x W^T + bias (dW = dz^T x, the
     residual's gradient is dy), its rows padded to 16 bytes where n is not a multiple of 8; for act "none" without gating
     it equals dy (may be dy itself) and preact may be None."""
-    device = dy.device
-    other = _on_device(device)
-    if other is not None:
-        with other:
-            return linear_backward(W, dy, preact, act, gated, need_dx, need_dbias, status)
     torch = _torch()
+    device = dy.device
+    if not _is_current(torch, device):
+        with torch.cuda.device(device):
+            return linear_backward(W, dy, preact, act, gated, need_dx, need_dbias, status)
     half = torch.float16
     if dy.dim() != 2:
         raise ValueError(f"dy: needs [m][n_out], got {list(dy.shape)}")
-    m, a = dy.shape[0], _act_id(act)
-    dy = _operand(dy, "dy", (m, W.n // 2 if gated else W.n), half, device)
+    m, n, a = dy.shape[0], W.n, _act_id(act)
+    dy = _operand(dy, "dy", (m, n // 2 if gated else n), half, device)
     c = _layer_matrix(W, "W", device)
     identity = a == 0 and not gated
     if preact is not None:
-        preact = _operand(preact, "preact", (m, W.n), half, device)
+        preact = _operand(preact, "preact", (m, n), half, device)
     elif not identity:
         raise ValueError(f"preact: needed for act {act!r} with gated={gated}")
-    dx = torch.empty((m, W.k), dtype=half, device=device) if need_dx else None
-    db = torch.empty((W.n,), dtype=torch.float32, device=device) if need_dbias else None
     if identity and not need_dx and not need_dbias:
         return None, dy, None
+    dx = dy.new_empty((m, W.k)) if need_dx else None
+    db = dy.new_empty((n,), dtype=torch.float32) if need_dbias else None
     # rows of dz are 16-byte aligned: padded (and for act "none" a copy of dy) where n is not a multiple of 8
-    own_dz = not identity or (need_dx and W.n % 8 != 0)
-    dz = torch.empty((m, (W.n + 7) // 8 * 8), dtype=half, device=device) if own_dz else dy
+    own_dz = not identity or (need_dx and n % 8 != 0)
+    stride = (n + 7) // 8 * 8 if own_dz else n
+    dz = dy.new_empty((m, stride)) if own_dz else dy
     st = lib().tern_linear_backward(c, dy.data_ptr(), preact.data_ptr() if preact is not None else None, m, a,
                                     1 if gated else 0, dx.data_ptr() if need_dx else None, dz.data_ptr() if own_dz else None,
-                                    dz.stride(0), db.data_ptr() if need_dbias else None,
-                                    status.data_ptr() if status is not None else None,
-                                    torch.cuda.current_stream().cuda_stream)
-    _check(st, "tern_linear_backward")
-    if own_dz and dz.shape[1] != W.n:
-        dz = dz[:, :W.n]
-    return dx, dz, db
+                                    stride, db.data_ptr() if need_dbias else None, _status_ptr(status, device),
+                                    _raw_stream(torch, device))
+    if st:
+        _check(st, "tern_linear_backward")
+    return dx, dz if stride == n else dz[:, :n], db
 
 
 def _moe_layer(gate_up, down, router, top_k, act, renormalize, device):
@@ -564,7 +579,7 @@ def moe_workspace_bytes(gate_up: TernMatrix, down: TernMatrix, router, tokens: i
 
 
 def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str = "silu", renormalize: bool = True,
-        residual=None, y=None, workspace=None, return_routing: bool = False, status=None):
+        residual=None, y=None, workspace=None, return_routing: bool = False):
     """A whole mixture-of-experts layer for up to MOE_MAX_TOKENS tokens (tern_moe): x fp16 [tokens][d] is routed by
     softmax(x router^T), router fp16 [experts][d], to the top_k most probable experts (ties to the lower index), and
     y = sum over them of p * down_e(act(gate_e x) * up_e x) (+ residual).
@@ -572,12 +587,11 @@ def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str =
     gate_up: packed [experts * 2f][d], for each expert f gate rows and then f up rows; down: packed [experts * d][f].
     workspace: a uint8 tensor of moe_workspace_bytes() (any contents; allocated when None). With return_routing
     returns (y, weights fp32 [tokens][top_k], ids int32 [tokens][top_k])."""
-    device = x.device
-    other = _on_device(device)
-    if other is not None:
-        with other:
-            return moe(gate_up, down, router, x, top_k, act, renormalize, residual, y, workspace, return_routing, status)
     torch = _torch()
+    device = x.device
+    if not _is_current(torch, device):
+        with torch.cuda.device(device):
+            return moe(gate_up, down, router, x, top_k, act, renormalize, residual, y, workspace, return_routing)
     half = torch.float16
     if x.dim() != 2 or router.dim() != 2:
         raise ValueError(f"x and router: need [tokens][d] and [experts][d], got {list(x.shape)} and {list(router.shape)}")
@@ -586,22 +600,26 @@ def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str =
     router = _operand(router, "router", (router.shape[0], d), half, device)
     layer = _moe_layer(gate_up, down, router, top_k, act, renormalize, device)
     if y is None:
-        y = torch.empty((tokens, d), dtype=half, device=device)
+        y = x.new_empty((tokens, d))
     else:
         _need(y, "y", (tokens, d), half, device)
     if residual is not None and residual is not y:
         residual = _operand(residual, "residual", (tokens, d), half, device)
+    l = lib()
     if workspace is None:
-        workspace = torch.empty(max(1, int(lib().tern_moe_workspace_bytes(layer, tokens))), dtype=torch.uint8, device=device)
+        size = l.tern_moe_workspace_bytes(layer, tokens) or 1
+        workspace = x.new_empty((size,), dtype=torch.uint8)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: needs a contiguous tensor on {device}")
-    weights = ids = None
+    else:
+        size = workspace.numel() * workspace.element_size()
+    weights = ids = wp = ip = None
     if return_routing:
-        weights = torch.empty((tokens, max(0, top_k)), dtype=torch.float32, device=device)
-        ids = torch.empty((tokens, max(0, top_k)), dtype=torch.int32, device=device)
-    st = lib().tern_moe(layer, x.data_ptr(), tokens, residual.data_ptr() if residual is not None else None, y.data_ptr(),
-                        weights.data_ptr() if return_routing else None, ids.data_ptr() if return_routing else None,
-                        workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                        status.data_ptr() if status is not None else None, torch.cuda.current_stream().cuda_stream)
-    _check(st, "tern_moe")
+        weights = x.new_empty((tokens, max(0, top_k)), dtype=torch.float32)
+        ids = x.new_empty((tokens, max(0, top_k)), dtype=torch.int32)
+        wp, ip = weights.data_ptr(), ids.data_ptr()
+    st = l.tern_moe(layer, x.data_ptr(), tokens, residual.data_ptr() if residual is not None else None, y.data_ptr(), wp, ip,
+                    workspace.data_ptr(), size, _raw_stream(torch, device))
+    if st:
+        _check(st, "tern_moe")
     return (y, weights, ids) if return_routing else y

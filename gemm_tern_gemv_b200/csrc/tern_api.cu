@@ -394,14 +394,13 @@ size_t tern_moe_workspace_bytes(const tern_moe_layer* layer, int64_t tokens) {
 }
 
 tern_status tern_moe(const tern_moe_layer* layer, const uint16_t* x, int64_t tokens, const uint16_t* residual, uint16_t* y,
-                     float* weights, int32_t* ids, void* workspace, size_t workspace_bytes, uint32_t* device_status,
-                     void* stream) {
+                     float* weights, int32_t* ids, void* workspace, size_t workspace_bytes, void* stream) {
   const tern_status s = check_moe(layer, tokens);
   if (s != TERN_OK) return s;
   if (!x || !y || !layer->router) return TERN_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(layer->router)) return TERN_ERR_ALIGNMENT;
   if (!aligned2(y) || !aligned2(residual) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
-      (reinterpret_cast<uintptr_t>(ids) & 3u) || (reinterpret_cast<uintptr_t>(device_status) & 3u))
+      (reinterpret_cast<uintptr_t>(ids) & 3u))
     return TERN_ERR_ALIGNMENT;
   const MoePlan plan = moe_plan(tokens, layer->gate_up->k, layer->down->k, layer->top_k);
   if (!workspace || workspace_bytes < plan.bytes) return TERN_ERR_WORKSPACE;

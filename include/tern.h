@@ -407,12 +407,11 @@ TERN_API size_t tern_moe_workspace_bytes(const tern_moe_layer* layer, int64_t to
  *   weights    device fp32 [tokens][top_k] or NULL;  ids  device int32 [tokens][top_k] or NULL
  *   workspace  device, >= tern_moe_workspace_bytes, 16-byte aligned, contents do not matter. Calls that
  *              share a workspace must not overlap on the GPU.
- *   device_status  device uint32 or NULL, as for tern_gemm
  * Errors: TERN_ERR_INVALID_ARG (also matrices whose shapes do not fit together), TERN_ERR_UNSUPPORTED
  * (layout, act, or a size over the limits above), TERN_ERR_ALIGNMENT, TERN_ERR_WORKSPACE, TERN_ERR_CUDA. */
 TERN_API tern_status tern_moe(const tern_moe_layer* layer, const uint16_t* x, int64_t tokens, const uint16_t* residual,
                               uint16_t* y, float* weights, int32_t* ids, void* workspace, size_t workspace_bytes,
-                              uint32_t* device_status, void* stream);
+                              void* stream);
 
 /* ---- activation-side block Hadamard rotation ------------------------------------------------ */
 

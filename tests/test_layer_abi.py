@@ -37,7 +37,7 @@ def test_bad_matrix(lib, kw, status):
     assert lib.tern_linear_backward(m, _p(FAKE), None, 1, 0, 0, _p(FAKE), None, 0, None, None, None) == status
     for g, d in ((m, ok), (ok, m)):
         layer = T.TernMoeLayerC(ctypes.pointer(g), ctypes.pointer(d), FAKE, 4, 2, 3, 1)
-        assert lib.tern_moe(layer, _p(FAKE), 1, None, _p(FAKE), None, None, _p(FAKE), 1 << 30, None, None) == status
+        assert lib.tern_moe(layer, _p(FAKE), 1, None, _p(FAKE), None, None, _p(FAKE), 1 << 30, None) == status
         assert lib.tern_moe_workspace_bytes(layer, 1) == 0
 
 
@@ -78,8 +78,8 @@ def test_moe_rejects_and_workspace(lib):
     dn = _mat(n=e * d, k=f)
     def layer(g=g, dn=dn, router=FAKE, experts=e, top_k=2, act=3, renorm=1):
         return T.TernMoeLayerC(ctypes.pointer(g), ctypes.pointer(dn), router, experts, top_k, act, renorm)
-    def call(lay, x=FAKE, tokens=3, res=None, y=FAKE, w=None, ids=None, ws=FAKE, wsb=1 << 30, status=None):
-        return lib.tern_moe(lay, _p(x), tokens, _p(res), _p(y), _p(w), _p(ids), _p(ws), wsb, _p(status), None)
+    def call(lay, x=FAKE, tokens=3, res=None, y=FAKE, w=None, ids=None, ws=FAKE, wsb=1 << 30):
+        return lib.tern_moe(lay, _p(x), tokens, _p(res), _p(y), _p(w), _p(ids), _p(ws), wsb, None)
     for kw, st in ((dict(experts=0), 1), (dict(experts=5), 1), (dict(top_k=0), 1), (dict(top_k=5), 1), (dict(act=6), 2),
                    (dict(renorm=2), 1), (dict(g=_mat(n=e * 2 * f + 2, k=d)), 1), (dict(dn=_mat(n=e * d, k=d)), 1),
                    (dict(router=0), 1), (dict(router=FAKE + 2), 3)):
@@ -87,7 +87,7 @@ def test_moe_rejects_and_workspace(lib):
     lay = layer()
     assert call(lay, x=0) == 1 and call(lay, y=0) == 1 and call(lay, tokens=0) == 1 and call(lay, tokens=65) == 2
     assert call(lay, x=FAKE + 8) == 3 and call(lay, y=FAKE + 1) == 3 and call(lay, w=FAKE + 2) == 3 and call(lay, ids=FAKE + 1) == 3
-    assert call(lay, status=FAKE + 2) == 3 and call(lay, res=FAKE + 1) == 3
+    assert call(lay, res=FAKE + 1) == 3
     need = lib.tern_moe_workspace_bytes(lay, 3)
     assert need > 0 and call(lay, ws=0) == 4 and call(lay, wsb=need - 1) == 4 and call(lay, ws=FAKE + 8) == 3
     assert lib.tern_moe_workspace_bytes(lay, 65) == 0 and lib.tern_moe_workspace_bytes(None, 1) == 0
