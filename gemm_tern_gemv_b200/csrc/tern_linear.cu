@@ -37,14 +37,14 @@ struct RowsParams {
   int tiles, tokens, early;
 };
 
-template <int L, int MODE, int NT>
+template <int L, class P>
 __global__ void __launch_bounds__(rows::kThreads, 1) linear_rows_kernel(const __grid_constant__ RowsParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   sm100::griddep_launch_dependents();
   if (!p.early) sm100::griddep_wait();
   const int t0 = (int)((int64_t)blockIdx.x * p.tiles / gridDim.x), t1 = (int)((int64_t)(blockIdx.x + 1) * p.tiles / gridDim.x);
   const rows::HalfRows xs{p.x, p.mat.K, nullptr};
-  rows::Product<L, MODE, NT> prod;
+  P prod;
   prod.run(smem, p.split, p.mat, p.map, t0, t1, xs, p.tokens, [&] { if (p.early) sm100::griddep_wait(); },
            [&](int tile, int r, int t, float z0, float z1) {
              epilogue(p.e, p.n, p.nout, t, (int64_t)tile * p.map.step + r, z0, z1, p.y);
@@ -53,14 +53,16 @@ __global__ void __launch_bounds__(rows::kThreads, 1) linear_rows_kernel(const __
 
 constexpr size_t kRoom = 227 * 1024;  // shared memory of a CTA
 
-template <int L, int MODE, int NT>
+template <int L, class P>
 cudaError_t launch_rows(RowsParams& p, cudaStream_t st) {
-  using P = rows::Product<L, MODE, NT>;
+  const int step = p.e.gated ? P::kTileRows / 2 : P::kTileRows;
+  p.map.step = step;
+  p.map.ahead = p.e.gated ? 0 : step / 2;
+  p.tiles = (int)((p.nout + step - 1) / step);
   const int grid = std::min(p.tiles, sm_count());
-  if (!rows::plan_split<P>((p.tiles + grid - 1) / grid, p.mat.units, kRoom, &p.split)) return cudaErrorInvalidValue;
+  if (!P::plan((p.tiles + grid - 1) / grid, p.mat.units, kRoom, &p.split)) return cudaErrorInvalidValue;
   const size_t smem = P::smem_bytes(p.split);
-  const void* kern = reinterpret_cast<const void*>(&linear_rows_kernel<L, MODE, NT>);
-  const cudaError_t err = allow_smem(kern, kRoom);
+  const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_rows_kernel<L, P>), kRoom);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)grid);
@@ -72,18 +74,19 @@ cudaError_t launch_rows(RowsParams& p, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, linear_rows_kernel<L, MODE, NT>, p);
+  return cudaLaunchKernelEx(&cfg, linear_rows_kernel<L, P>, p);
 }
 
-// m <= 2: the int8 form; otherwise fp16 column tiles of 8 rows of x (4 with two slots per unit).
+// m <= 2: int8 digits with the operands in registers; otherwise fp16 column tiles of 8 rows of x (4 with two
+// slots per unit).
 template <int L>
 cudaError_t pick_rows(RowsParams& p, cudaStream_t st) {
-  if (p.tokens <= rows::Geo<L, rows::kInt8>::kTok) return launch_rows<L, rows::kInt8, 1>(p, st);
-  if (p.tokens <= 2) return launch_rows<L, rows::kInt8, 2>(p, st);
+  if (p.tokens == 1) return launch_rows<L, rows::Product<L, rows::kInt8, 1>>(p, st);
+  if (p.tokens == 2) return launch_rows<L, rows::Product<L, rows::kInt8, 2 / rows::Geo<L, rows::kInt8>::kTok>>(p, st);
   const int nt = (p.tokens + rows::Geo<L, rows::kFp16>::kTok - 1) / rows::Geo<L, rows::kFp16>::kTok;
-  if (nt == 1) return launch_rows<L, rows::kFp16, 1>(p, st);
-  if (nt == 2) return launch_rows<L, rows::kFp16, 2>(p, st);
-  return launch_rows<L, rows::kFp16, 4>(p, st);
+  if (nt == 1) return launch_rows<L, rows::Product<L, rows::kFp16, 1>>(p, st);
+  if (nt == 2) return launch_rows<L, rows::Product<L, rows::kFp16, 2>>(p, st);
+  return launch_rows<L, rows::Product<L, rows::kFp16, 4>>(p, st);
 }
 
 constexpr int kFewRows = 16;
@@ -97,13 +100,12 @@ cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, ui
     RowsParams p{};
     p.mat = rows::Mat{static_cast<const uint8_t*>(W.codes), W.scales, W.code_row_stride, W.scale_row_stride, (int)W.k,
                       (int)row_bytes(W.layout, W.k), (int)(W.k / kGroup), (int)((row_bytes(W.layout, W.k) + 31) / 32)};
-    p.map = e.gated ? rows::Map{0, nout, (int)nout, 8, 0} : rows::Map{0, 0, (int)nout, 16, 8};
+    p.map = rows::Map{0, e.gated ? nout : 0, (int)nout, 0, 0};
     p.x = x;
     p.y = y;
     p.e = e;
     p.n = W.n;
     p.nout = nout;
-    p.tiles = (int)((nout + p.map.step - 1) / p.map.step);
     p.tokens = (int)m;
     p.early = (flags & TERN_GEMV_STATIC_WEIGHTS) ? 1 : 0;
     switch (W.layout) {

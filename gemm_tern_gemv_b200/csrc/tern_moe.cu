@@ -8,7 +8,7 @@
 //          the first collects them through the cluster's shared memory and picks.
 //   up     the (token, expert) pairs are sorted by expert; the 8-output tiles (gate and up rows) of all experts
 //          in use form one list that is dealt evenly to one CTA per SM. The products are those of
-//          tern_rows.cuh: int8 digits for one or two tokens of an expert, fp16 for more. h = act(g) u in fp32.
+//          tern_rows.cuh. h = act(g) u in fp32.
 //   down   the same over 16-row tiles of the down matrices, with h brought into fp16's range by a power of two
 //          per pair. Sums of a pair go to the workspace; whoever finishes a 16-column strip of y last (a counter
 //          per strip) adds its pairs up in the order of j, so the result does not depend on who that was.
@@ -34,12 +34,11 @@ __device__ __forceinline__ void store_first(double* local, double v) {  // into 
   asm volatile("st.shared::cluster.f64 [%0], %1;" ::"r"(remote), "d"(v) : "memory");
 }
 
-// Whether logit a of expert ia goes before logit b of ib: larger first, ties to the lower index, NaN last.
-__device__ __forceinline__ bool before(double a, int ia, double b, int ib) {
-  const bool na = a != a, nb = b != b;
-  if (na != nb) return nb;
-  if (!na && a != b) return a > b;
-  return ia < ib;
+// 64-bit key whose unsigned order is that of the doubles, -0 as 0, any NaN below everything (and above 0 = none).
+__device__ __forceinline__ uint64_t order_key(double v) {
+  if (v != v) return 1;
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  return b >> 63 ? ~b : b | 1ull << 63;
 }
 
 // e^d with d's rounding to fp32 made good: e^(hi + lo) = e^hi (1 + lo).
@@ -59,12 +58,12 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
   const int rank = (int)cluster_rank();
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
-  for (int i = (int)(blockIdx.x * kRouteThreads + threadIdx.x); i < p.tokens * p.top_k + p.d / 16; i += (int)gridDim.x * kRouteThreads)
+  for (int i = (int)(blockIdx.x * kRouteThreads + threadIdx.x); i < p.tokens * p.top_k + p.d / 8; i += (int)gridDim.x * kRouteThreads)
     p.clear[i] = 0;  // largest |h| of each pair, then the strips' counters
   for (int e = rank + kRouteCtas * warp; e < p.experts; e += kRouteCtas * (kRouteThreads / 32)) {
-    double s[TOK] = {};
+    double s[TOK][4] = {};  // four sums each: fp64 additions take long one after the other
     const uint4* w = reinterpret_cast<const uint4*>(p.router + (int64_t)e * p.d);
-#pragma unroll 2
+#pragma unroll 4
     for (int v = lane; v < p.d / 8; v += 32) {
       const uint4 a = __ldg(w + v);
       const uint32_t av[4] = {a.x, a.y, a.z, a.w};
@@ -76,148 +75,153 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
 #pragma unroll
         for (int q = 0; q < 4; q++) {
           const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&av[q])), y = __half22float2(*reinterpret_cast<const __half2*>(&bv[q]));
-          s[i] += (double)(x.x * y.x);
-          s[i] += (double)(x.y * y.y);
+          s[i][q] += (double)(x.x * y.x);
+          s[i][q] += (double)(x.y * y.y);
         }
       }
     }
 #pragma unroll
     for (int i = 0; i < TOK; i++) {
-      for (int o = 16; o; o >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-      if (lane == 0) store_first(&logit[i][e], s[i]);
+      double v = (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+      for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      if (lane == 0) store_first(&logit[i][e], v);
     }
   }
   cluster_sync();
   if (rank || warp >= TOK || t0 + warp >= p.tokens) return;
-  // one warp per token: lane l holds the logits of experts l, l + 32, ...
-  const int t = t0 + warp;
-  constexpr int kPer = kMoeMaxExperts / 32;
-  double l[kPer];
+  // One warp per token; lane l holds the logits of experts l, l + 32, ... as 64-bit keys whose unsigned order
+  // is the logits' (NaN last). Each pick is three warp reductions: high word, low word, lowest index.
+  const int t = t0 + warp, per = (p.experts + 31) / 32;
   double mx = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < kPer; i++) {
-    l[i] = lane + 32 * i < p.experts ? logit[warp][lane + 32 * i] : -INFINITY;
-    mx = fmax(mx, l[i]);
-  }
+  for (int i = 0; i < per; i++)
+    if (lane + 32 * i < p.experts) mx = fmax(mx, logit[warp][lane + 32 * i]);
   for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
   float sum = 0.f;
-#pragma unroll
-  for (int i = 0; i < kPer; i++)
-    if (lane + 32 * i < p.experts) sum += exp_exact(l[i] - mx);
+  for (int i = 0; i < per; i++)
+    if (lane + 32 * i < p.experts) sum += exp_exact(logit[warp][lane + 32 * i] - mx);
   for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   uint32_t used = 0;  // bit i: expert lane + 32 i is taken
   float chosen = 0.f, mine = 0.f;
+  uint64_t best = 0;
+  int be = -1;
+  bool stale = true;  // the lane's best is to be looked for
   for (int j = 0; j < p.top_k; j++) {
-    double best = 0.;
-    int be = kMoeMaxExperts + lane;  // none
-    bool has = false;
-#pragma unroll
-    for (int i = 0; i < kPer; i++) {
-      const int e = lane + 32 * i;
-      if (e < p.experts && !(used >> i & 1) && (!has || before(l[i], e, best, be))) {
-        best = l[i];
-        be = e;
-        has = true;
+    if (stale) {
+      best = 0;
+      be = -1;
+      for (int i = 0; i < per; i++) {
+        const int e = lane + 32 * i;
+        if (e >= p.experts || (used >> i & 1)) continue;
+        const uint64_t k = order_key(logit[warp][e]);
+        if (be < 0 || k > best) {
+          best = k;
+          be = e;
+        }
       }
+      stale = false;
     }
-    for (int o = 16; o; o >>= 1) {
-      const double ob = __shfl_xor_sync(0xffffffffu, best, o);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, o);
-      const bool oh = oe < kMoeMaxExperts;
-      if (oh && (be >= kMoeMaxExperts || before(ob, oe, best, be))) {
-        best = ob;
-        be = oe;
-      }
+    const uint32_t hi = be >= 0 ? (uint32_t)(best >> 32) : 0u, top = __reduce_max_sync(0xffffffffu, hi);
+    const bool in = be >= 0 && hi == top;
+    const uint32_t low = __reduce_max_sync(0xffffffffu, in ? (uint32_t)best : 0u);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, in && (uint32_t)best == low ? (uint32_t)be : 0xffffu);
+    if ((int)e == be) {
+      used |= 1u << (e >> 5);
+      stale = true;
     }
-    if ((be & 31) == lane) used |= 1u << (be >> 5);
-    const float w = exp_exact(best - mx) / sum;
+    const float w = exp_exact(logit[warp][e] - mx) / sum;
     chosen += w;
     if (lane == j) {
       mine = w;
-      p.ids[t * p.top_k + j] = be;
+      p.ids[t * p.top_k + j] = (int)e;
     }
   }
   if (lane < p.top_k) p.weights[t * p.top_k + lane] = p.renormalize ? mine / chosen : mine;
 }
 
 // ---- the experts ------------------------------------------------------------------------------------------
-// Columns of a chunk: pairs of one expert that go through its weights together.
-template <int L> constexpr int chunk() { return 2 * rows::Geo<L, rows::kFp16>::kTok; }
+// The form of the product is the same for all experts of a call (side by side in one kernel the forms would
+// share their registers): int8 digits for one or two tokens; fp16 column tiles for more, one of them, or two
+// where an expert gets six tokens or more on average. P::kRows pairs of an expert go through its weights
+// together.
 constexpr int kPlans = 8;  // cuts for up to 1, 2, 3, 4, 6, 8, 16 and any number of tiles
 __host__ __device__ constexpr int plan_tiles(int i) { return i < 4 ? i + 1 : i == 4 ? 6 : i == 5 ? 8 : i == 6 ? 16 : 32; }
-enum Variant { kOne8, kTwo8, kOne16, kTwo16, kVariants };  // int8 with one or two column tiles, fp16 likewise
-struct Plans {
-  rows::Split split[kVariants][kPlans];
-};
+
+constexpr int kMaxStrips = 128;  // strips (row tiles of the down matrix) between two looks at their counters
 
 struct Lists {
-  int segments, tiles;             // chunks of pairs; 16-row tiles of all of them
+  int segments, tiles;             // chunks of pairs; row tiles of all of them
   uint16_t pair[kMaxPairs];        // pairs sorted by expert
+  uint16_t unsorted[kMaxPairs];
   uint16_t seg_expert[kMaxPairs], seg_first[kMaxPairs];
   uint8_t seg_count[kMaxPairs];
-  uint16_t expert[kMaxPairs];      // of each pair, in the pairs' own order
   int count[kMoeMaxExperts], first[kMoeMaxExperts];
+  uint32_t total[kMoeMaxExperts / 32];
   int index[16];                   // rows of the activations of the current segment
   float mul[16];                   // and their powers of two
-  int last[64];                    // strips that this CTA finished
+  int last[kMaxStrips];            // strips that this CTA finished
 };
 
-// Sorts the pairs by expert (in the pairs' order within an expert) and cuts them into segments.
-__device__ void build_lists(const MoeParams& p, Lists& s, int cols, int tiles_per_segment) {
-  const int tid = threadIdx.x, lane = tid & 31, pairs = p.tokens * p.top_k;
-  for (int i = tid; i < pairs; i += rows::kThreads) s.expert[i] = (uint16_t)p.ids[i];
-  for (int i = tid; i < kMoeMaxExperts; i += rows::kThreads) s.count[i] = 0;
+// Sorts the pairs by expert, in their own order within it (every CTA has to cut the same segments), and cuts
+// them into segments of at most `cols`.
+__device__ __forceinline__ void build_lists(const MoeParams& p, Lists& s, int cols, int tiles_per_segment) {
+  constexpr int kPer = kMaxPairs / rows::kThreads, kWarps = kMoeMaxExperts / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pairs = p.tokens * p.top_k;
+  int e[kPer], place[kPer];
+  if (tid < kMoeMaxExperts) s.count[tid] = 0;
+#pragma unroll
+  for (int c = 0; c < kPer; c++) e[c] = tid + c * rows::kThreads < pairs ? p.ids[tid + c * rows::kThreads] : -1;
   __syncthreads();
-  if (tid < 32) {
-    for (int i0 = 0; i0 < pairs; i0 += 32) {
-      const int i = i0 + lane, e = i < pairs ? (int)s.expert[i] : kMoeMaxExperts + lane;
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      if (i < pairs) {
-        const int base = s.count[e];
-        s.pair[i] = (uint16_t)(base + __popc(same & ((1u << lane) - 1u)));  // its place among the expert's pairs
-        __syncwarp(__activemask());
-        if (lane == __ffs(same) - 1) s.count[e] = base + __popc(same);
-      }
-      __syncwarp();
+#pragma unroll
+  for (int c = 0; c < kPer; c++)
+    if (e[c] >= 0) place[c] = atomicAdd(&s.count[e[c]], 1);
+  __syncthreads();
+  // prefix sums over the experts: pairs in the low, segments in the high half of a word
+  uint32_t n = 0, g = 0, sum = 0;
+  if (tid < kMoeMaxExperts) {
+    n = (uint32_t)s.count[tid];
+    g = (n + cols - 1) / cols;
+    sum = n | g << 16;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += v;
     }
-    int before = 0, segs = 0;
-    for (int e0 = 0; e0 < kMoeMaxExperts; e0 += 32) {
-      const int n = s.count[e0 + lane], g = (n + cols - 1) / cols;
-      int a = n, b = g;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, a, o), y = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane >= o) {
-          a += x;
-          b += y;
-        }
-      }
-      s.first[e0 + lane] = before + a - n;
-      for (int i = 0, at = segs + b - g; i < g; i++, at++) {
-        s.seg_expert[at] = (uint16_t)(e0 + lane);
-        s.seg_first[at] = (uint16_t)(before + a - n + i * cols);
-        s.seg_count[at] = (uint8_t)min(cols, n - i * cols);
-      }
-      before += __shfl_sync(0xffffffffu, a, 31);
-      segs += __shfl_sync(0xffffffffu, b, 31);
+    if (lane == 31) s.total[warp] = sum;
+  }
+  __syncthreads();
+  if (tid < kMoeMaxExperts) {
+    uint32_t all = 0, base = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      const uint32_t v = s.total[w];
+      if (w < warp) base += v;
+      all += v;
     }
-    if (lane == 0) {
-      s.segments = segs;
-      s.tiles = segs * tiles_per_segment;
+    const uint32_t at = base + sum - (n | g << 16);
+    s.first[tid] = (int)(at & 0xffff);
+    for (uint32_t i = 0; i < g; i++) {
+      s.seg_expert[(at >> 16) + i] = (uint16_t)tid;
+      s.seg_first[(at >> 16) + i] = (uint16_t)((at & 0xffff) + i * cols);
+      s.seg_count[(at >> 16) + i] = (uint8_t)min((uint32_t)cols, n - i * cols);
+    }
+    if (tid == 0) {
+      s.segments = (int)(all >> 16);
+      s.tiles = (int)(all >> 16) * tiles_per_segment;
     }
   }
   __syncthreads();
-  // every pair to its place: read the places first, they share the array
-  uint16_t at[kMaxPairs / rows::kThreads];
 #pragma unroll
-  for (int c = 0; c < kMaxPairs / rows::kThreads; c++) {
-    const int i = tid + c * rows::kThreads;
-    at[c] = i < pairs ? (uint16_t)(s.first[s.expert[i]] + s.pair[i]) : (uint16_t)0;
-  }
+  for (int c = 0; c < kPer; c++)
+    if (e[c] >= 0) s.unsorted[s.first[e[c]] + place[c]] = (uint16_t)(tid + c * rows::kThreads);
   __syncthreads();
 #pragma unroll
-  for (int c = 0; c < kMaxPairs / rows::kThreads; c++) {
-    const int i = tid + c * rows::kThreads;
-    if (i < pairs) s.pair[at[c]] = (uint16_t)i;
+  for (int c = 0; c < kPer; c++) {
+    if (e[c] < 0) continue;
+    const int me = tid + c * rows::kThreads, first = s.first[e[c]], of = s.count[e[c]];
+    int rank = 0;
+#pragma unroll 4
+    for (int i = 0; i < of; i++) rank += s.unsorted[first + i] < me;
+    s.pair[first + rank] = (uint16_t)me;
   }
   __syncthreads();
 }
@@ -225,93 +229,78 @@ __device__ void build_lists(const MoeParams& p, Lists& s, int cols, int tiles_pe
 struct ExpertParams {
   MoeParams p;
   rows::Mat mat;
-  Plans plans;
+  rows::Split split[kPlans];
 };
-
-// Tiles [a, b) of segment g in one form of the product. Out of line: inlined side by side, the forms would
-// share their registers.
-template <int L, bool UP, int MODE, int NT>
-__device__ __noinline__ void run_form(uint8_t* smem, const ExpertParams* q, const Lists* s, int form, int g, int a, int b) {
-  const MoeParams& p = q->p;
-  int plan = 0;
-  while (plan < kPlans - 1 && plan_tiles(plan) < b - a) plan++;
-  const uint16_t* pair = s->pair + s->seg_first[g];
-  const int n = s->seg_count[g];
-  const auto none = [] {};
-  rows::Product<L, MODE, NT> prod;
-  if constexpr (UP) {
-    const int64_t first = (int64_t)s->seg_expert[g] * 2 * p.f;
-    prod.run(smem, q->plans.split[form][plan], q->mat, rows::Map{first, first + p.f, p.f, 8, 0}, a, b, rows::HalfRows{p.x, p.d, s->index},
-             n, none, [&](int tile, int r, int c, float gate, float up) {
-               const float h = act_fwd(p.act, gate) * up;
-               const int pr = pair[c];
-               p.h[(int64_t)pr * p.f + tile * 8 + r] = h;
-               // largest |h| of the pair, as bits: order does not matter to a maximum. NaN counts as the largest.
-               atomicMax(p.clear + pr, __float_as_uint(h) & 0x7fffffffu);
-             });
-  } else {
-    const int64_t first = (int64_t)s->seg_expert[g] * p.d;
-    prod.run(smem, q->plans.split[form][plan], q->mat, rows::Map{first, first, p.d, 16, 8}, a, b,
-             rows::FloatRows{p.h, p.f, s->index, s->mul}, n, none, [&](int tile, int r, int c, float z, float) {
-               p.z[(int64_t)pair[c] * p.d + tile * 16 + r] = MODE == rows::kFp16 ? z / s->mul[c] : z;
-             });
-  }
+__device__ __forceinline__ const rows::Split& split_for(const ExpertParams& q, int tiles) {
+  int i = 0;
+  while (i < kPlans - 1 && plan_tiles(i) < tiles) i++;
+  return q.split[i];
 }
 
-template <int L, bool UP>
-__device__ __forceinline__ void run_segment(uint8_t* smem, const ExpertParams* q, const Lists* s, int g, int a, int b) {
-  constexpr int k8 = rows::Geo<L, rows::kInt8>::kTok, k16 = rows::Geo<L, rows::kFp16>::kTok;
-  const int n = s->seg_count[g];
-  if (n <= k8) run_form<L, UP, rows::kInt8, 1>(smem, q, s, kOne8, g, a, b);
-  else if (n <= 2) run_form<L, UP, rows::kInt8, k8 < 2 ? 2 : 1>(smem, q, s, kTwo8, g, a, b);
-  else if (n <= k16) run_form<L, UP, rows::kFp16, 1>(smem, q, s, kOne16, g, a, b);
-  else run_form<L, UP, rows::kFp16, 2>(smem, q, s, kTwo16, g, a, b);
-}
-
-template <int L>
+template <int L, class P>
 __global__ void __launch_bounds__(rows::kThreads, 1) moe_up_kernel(const __grid_constant__ ExpertParams q) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Lists s;
   const MoeParams& p = q.p;
+  constexpr int kStep = P::kTileRows / 2;
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
-  const int per = p.f / 8;  // tiles of a segment
-  build_lists(p, s, chunk<L>(), per);
+  const int per = p.f / kStep;  // tiles of a segment
+  build_lists(p, s, P::kRows, per);
   const int t1 = (int)((int64_t)(blockIdx.x + 1) * s.tiles / gridDim.x);
+#pragma unroll 1
   for (int t = (int)((int64_t)blockIdx.x * s.tiles / gridDim.x); t < t1;) {
     const int g = t / per, a = t % per, b = min(per, a + t1 - t), n = s.seg_count[g];
     const uint16_t* pair = s.pair + s.seg_first[g];
     if ((int)threadIdx.x < n) s.index[threadIdx.x] = pair[threadIdx.x] / p.top_k;
     __syncthreads();
-    run_segment<L, true>(smem, &q, &s, g, a, b);
+    const int64_t first = (int64_t)s.seg_expert[g] * 2 * p.f;
+    P prod;
+    prod.run(smem, split_for(q, b - a), q.mat, rows::Map{first, first + p.f, p.f, kStep, 0}, a, b, rows::HalfRows{p.x, p.d, s.index},
+             n, [] {}, [&](int tile, int r, int c, float gate, float up) {
+               const float h = act_fwd(p.act, gate) * up;
+               const int pr = pair[c];
+               p.h[(int64_t)pr * p.f + tile * kStep + r] = h;
+               // largest |h| of the pair, as bits: order does not matter to a maximum. NaN counts as the largest.
+               if (P::kMode == rows::kFp16) atomicMax(p.clear + pr, __float_as_uint(h) & 0x7fffffffu);
+             });
     __syncthreads();
     t += b - a;
   }
 }
 
-template <int L>
+template <int L, class P>
 __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __grid_constant__ ExpertParams q) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Lists s;
   const MoeParams& p = q.p;
+  constexpr int kStep = P::kTileRows;
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
-  const int per = p.d / 16, tid = threadIdx.x;
-  build_lists(p, s, chunk<L>(), per);
+  const int per = p.d / kStep, tid = threadIdx.x;
+  build_lists(p, s, P::kRows, per);
   uint32_t* counter = p.clear + p.tokens * p.top_k;
   const int t1 = (int)((int64_t)(blockIdx.x + 1) * s.tiles / gridDim.x);
+#pragma unroll 1
   for (int t = (int)((int64_t)blockIdx.x * s.tiles / gridDim.x); t < t1;) {
-    const int g = t / per, a = t % per, b = min(min(per, a + t1 - t), a + 64), n = s.seg_count[g];
+    const int g = t / per, a = t % per, b = min(min(per, a + t1 - t), a + kMaxStrips), n = s.seg_count[g];
     const uint16_t* pair = s.pair + s.seg_first[g];
     if (tid < n) {
       const int pr = pair[tid];
-      const uint32_t top = p.clear[pr];
       s.index[tid] = pr;
-      // the fp16 form takes h times a power of two that brings the pair's largest to [2^14, 2^15)
-      s.mul[tid] = top == 0 || top >= 0x7f800000u ? 1.f : rows::exp2i(min(100, 15 - rows::exponent(top)));
+      if (P::kMode == rows::kFp16) {
+        // the fp16 form takes h times a power of two that brings the pair's largest to [2^14, 2^15)
+        const uint32_t top = p.clear[pr];
+        s.mul[tid] = top == 0 || top >= 0x7f800000u ? 1.f : rows::exp2i(min(100, 15 - rows::exponent(top)));
+      }
     }
     __syncthreads();
-    run_segment<L, false>(smem, &q, &s, g, a, b);
+    const int64_t first = (int64_t)s.seg_expert[g] * p.d;
+    P prod;
+    prod.run(smem, split_for(q, b - a), q.mat, rows::Map{first, first, p.d, kStep, kStep / 2}, a, b,
+             rows::FloatRows{p.h, p.f, s.index, s.mul}, n, [] {}, [&](int tile, int r, int c, float z, float) {
+               p.z[(int64_t)pair[c] * p.d + tile * kStep + r] = P::kMode == rows::kFp16 ? z / s.mul[c] : z;
+             });
     // strips that now have the sums of every segment
     __syncthreads();
     if (tid < b - a) {
@@ -320,13 +309,14 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
       __threadfence();
     }
     __syncthreads();
-    for (int i = tid; i < (b - a) * 16 * p.tokens; i += rows::kThreads) {
-      const int r = i % 16, tl = i / 16 % (b - a), tok = i / (16 * (b - a));
+    for (int i = tid; i < (b - a) * kStep * p.tokens; i += rows::kThreads) {
+      const int r = i % kStep, tl = i / kStep % (b - a), tok = i / (kStep * (b - a));
       if (!s.last[tl]) continue;
-      const int o = (a + tl) * 16 + r;
-      float y = 0.f;
-      for (int j = 0; j < p.top_k; j++) y = fmaf(p.weights[tok * p.top_k + j], __ldcg(p.z + (int64_t)(tok * p.top_k + j) * p.d + o), y);
+      const int o = (a + tl) * kStep + r;
       const int64_t at = (int64_t)tok * p.d + o;
+      float y = 0.f;
+#pragma unroll 4
+      for (int j = 0; j < p.top_k; j++) y = fmaf(p.weights[tok * p.top_k + j], __ldcg(p.z + (int64_t)(tok * p.top_k + j) * p.d + o), y);
       if (p.residual) y += h2f(p.residual[at]);
       p.y[at] = f2h(y);
     }
@@ -336,16 +326,6 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
 }
 
 constexpr size_t kRoom = 227 * 1024 - (sizeof(Lists) + 1023) / 1024 * 1024 - 1024;  // dynamic shared memory
-
-template <int L, int MODE, int NT>
-bool plan_variant(int units, rows::Split* out, size_t* smem) {
-  using P = rows::Product<L, MODE, NT>;
-  for (int i = 0; i < kPlans; i++) {
-    if (!rows::plan_split<P>(plan_tiles(i), units, kRoom, out + i)) return false;
-    *smem = std::max(*smem, P::smem_bytes(out[i]));
-  }
-  return true;
-}
 
 cudaError_t launch(const void* kern, int grid, int threads, size_t smem, cudaStream_t st, void* arg) {
   cudaLaunchConfig_t cfg{};
@@ -362,22 +342,29 @@ cudaError_t launch(const void* kern, int grid, int threads, size_t smem, cudaStr
   return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
-template <int L, bool UP>
-cudaError_t launch_experts(const tern_matrix& W, const MoeParams& p, cudaStream_t st) {
+template <int L, bool UP, class P>
+cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t st) {
   ExpertParams q;
   q.p = p;
   q.mat = rows::Mat{static_cast<const uint8_t*>(W.codes), W.scales, W.code_row_stride, W.scale_row_stride, (int)W.k,
                     (int)row_bytes(W.layout, W.k), (int)(W.k / kGroup), (int)((row_bytes(W.layout, W.k) + 31) / 32)};
   size_t smem = 0;
-  const bool ok = plan_variant<L, rows::kInt8, 1>(q.mat.units, q.plans.split[kOne8], &smem) &&
-                  plan_variant<L, rows::kInt8, L == TERN_Q2_0_G128 ? 1 : 2>(q.mat.units, q.plans.split[kTwo8], &smem) &&
-                  plan_variant<L, rows::kFp16, 1>(q.mat.units, q.plans.split[kOne16], &smem) &&
-                  plan_variant<L, rows::kFp16, 2>(q.mat.units, q.plans.split[kTwo16], &smem);
-  if (!ok) return cudaErrorInvalidValue;
-  const void* kern = UP ? reinterpret_cast<const void*>(&moe_up_kernel<L>) : reinterpret_cast<const void*>(&moe_down_kernel<L>);
+  for (int i = 0; i < kPlans; i++) {
+    if (!P::plan(plan_tiles(i), q.mat.units, kRoom, q.split + i)) return cudaErrorInvalidValue;
+    smem = std::max(smem, P::smem_bytes(q.split[i]));
+  }
+  const void* kern = UP ? reinterpret_cast<const void*>(&moe_up_kernel<L, P>) : reinterpret_cast<const void*>(&moe_down_kernel<L, P>);
   const cudaError_t e = allow_smem(kern, kRoom);
   if (e != cudaSuccess) return e;
   return launch(kern, sm_count(), rows::kThreads, smem, st, &q);
+}
+
+template <int L, bool UP>
+cudaError_t launch_experts(const tern_matrix& W, const MoeParams& p, cudaStream_t st) {
+  if (p.tokens == 1) return launch_form<L, UP, rows::Product<L, rows::kInt8, 1>>(W, p, st);
+  if (p.tokens == 2) return launch_form<L, UP, rows::Product<L, rows::kInt8, 2 / rows::Geo<L, rows::kInt8>::kTok>>(W, p, st);
+  if (p.tokens * p.top_k < 6 * p.experts) return launch_form<L, UP, rows::Product<L, rows::kFp16, 1>>(W, p, st);
+  return launch_form<L, UP, rows::Product<L, rows::kFp16, 2>>(W, p, st);
 }
 
 template <bool UP>
@@ -398,7 +385,7 @@ MoePlan moe_plan(int64_t tokens, int64_t d, int64_t f, int top_k) {
   auto take = [&](size_t bytes) { const size_t at = o; o += (bytes + 255) / 256 * 256; return at; };
   w.ids = take(pairs * 4);
   w.weights = take(pairs * 4);
-  w.clear = take((pairs + d / 16) * 4);
+  w.clear = take((pairs + d / 8) * 4);
   w.h = take(pairs * f * 4);
   w.z = take(pairs * d * 4);
   w.bytes = o;

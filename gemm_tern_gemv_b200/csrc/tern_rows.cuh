@@ -308,6 +308,44 @@ struct Split {
 // are one base and constant offsets, and a lane's scales of a row come in one or two loads.
 constexpr int kBlk = 4;
 
+// Code operands a0 .. a3 of each int8 MMA from 8 bytes of rows g (a) and g + 8 (b). k85, kc80: 85 and 80 in
+// both halves, opaque to the compiler so that the base-3 steps stay multiplications.
+template <int L>
+__device__ __forceinline__ void operands8(uint2 a, uint2 b, uint32_t k85, uint32_t kc80, uint32_t (&F)[4][Geo<L, kInt8>::kPairs * 2]) {
+  const uint32_t w[4] = {a.x, b.x, a.y, b.y};
+#pragma unroll
+  for (int i = 0; i < 4; i++) {
+    if constexpr (L == TERN_Q2_0_G128) {
+      const uint32_t z = w[i] >> 4;
+      F[i][0] = (w[i] ^ 0xAAAAAAAAu) & 0x03030303u;
+      F[i][1] = (w[i] ^ 0xAAAAAAAAu) & 0x0C0C0C0Cu;
+      F[i][2] = (z ^ 0xAAAAAAAAu) & 0x03030303u;
+      F[i][3] = (z ^ 0xAAAAAAAAu) & 0x0C0C0C0Cu;
+    } else if constexpr (L == TERN_Q1_0_G128) {
+      const uint32_t z = w[i] >> 4;
+#pragma unroll
+      for (int j = 0; j < 4; j++) {
+        F[i][j] = w[i] & (0x01010101u << j);
+        F[i][4 + j] = z & (0x01010101u << j);
+      }
+    } else {
+      uint32_t E = w[i] & 0x00FF00FFu, O = __byte_perm(w[i], 0u, 0x4341);
+      F[i][0] = w[i];
+#pragma unroll
+      for (int j = 1; j <= 4; j++) {
+        E = E * k85 + kc80;
+        O = O * k85 + kc80;
+        F[i][j] = __byte_perm(E, O, 0x7351);
+        if (j < 4) {
+          E = __byte_perm(E, 0u, 0x4341);
+          O = __byte_perm(O, 0u, 0x4341);
+        }
+      }
+      F[i][5] = 0;
+    }
+  }
+}
+
 template <int L, int MODE, int NT>
 struct Product {
   using T = Lay<L>;
@@ -316,6 +354,8 @@ struct Product {
   static constexpr int kDepth = 2;                       // blocks requested ahead by a warp
   static constexpr int kUnitBytes = NT * G::kTileBytes;  // activation operands of one unit
   static constexpr int kAcc = MODE == kInt8 ? 2 : 4;
+  static constexpr int kTileRows = 16, kMode = MODE;
+  static bool plan(int tiles, int units, size_t room, Split* out);
 
   // shared memory: operands [pass], partial sums [batch][wk][16][kRows], scratch [warps][256 words], flags
   static __host__ __device__ size_t part_bytes(const Split& s) { return (size_t)s.batch * s.wk * 16 * kRows * 4; }
@@ -397,7 +437,6 @@ struct Product {
   __device__ __forceinline__ void unit(uint2 a, uint2 b, float s0, float s1, uint32_t base, uint32_t hd, const uint32_t (&ent)[NT],
                                        float (&acc)[NT][kAcc]) {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-    const uint32_t w[4] = {a.x, b.x, a.y, b.y};
     if constexpr (MODE == kInt8) {
       int c[NT][4];
       float sc[NT];
@@ -414,44 +453,8 @@ struct Product {
         }
         sc[n] = __uint_as_float(r.z);
       }
-      uint32_t F[4][G::kPairs * 2];  // code operands a0 .. a3 of each MMA
-      if constexpr (L == TERN_Q2_0_G128) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint32_t z = w[i] >> 4;
-          F[i][0] = (w[i] ^ 0xAAAAAAAAu) & 0x03030303u;
-          F[i][1] = (w[i] ^ 0xAAAAAAAAu) & 0x0C0C0C0Cu;
-          F[i][2] = (z ^ 0xAAAAAAAAu) & 0x03030303u;
-          F[i][3] = (z ^ 0xAAAAAAAAu) & 0x0C0C0C0Cu;
-        }
-      } else if constexpr (L == TERN_Q1_0_G128) {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          const uint32_t z = w[i] >> 4;
-#pragma unroll
-          for (int j = 0; j < 4; j++) {
-            F[i][j] = w[i] & (0x01010101u << j);
-            F[i][4 + j] = z & (0x01010101u << j);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-          uint32_t E = w[i] & 0x00FF00FFu, O = __byte_perm(w[i], 0u, 0x4341);
-          F[i][0] = w[i];
-#pragma unroll
-          for (int j = 1; j <= 4; j++) {
-            E = E * k85 + kc80;
-            O = O * k85 + kc80;
-            F[i][j] = __byte_perm(E, O, 0x7351);
-            if (j < 4) {
-              E = __byte_perm(E, 0u, 0x4341);
-              O = __byte_perm(O, 0u, 0x4341);
-            }
-          }
-          F[i][5] = 0;
-        }
-      }
+      uint32_t F[4][G::kPairs * 2];
+      operands8<L>(a, b, k85, kc80, F);
 #pragma unroll
       for (int p = 0; p < G::kPairs; p++)
 #pragma unroll
@@ -473,6 +476,7 @@ struct Product {
         acc[n][1] = fmaf(s1 * sc[n], (float)v1, acc[n][1]);
       }
     } else {
+      const uint32_t w[4] = {a.x, b.x, a.y, b.y};
       float c[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; n++) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
@@ -582,6 +586,7 @@ struct Product {
     const uint32_t base0 = sm100::smem_u32(frag);
     const uint32_t hd0 = base0 + (uint32_t)(G::kPairs * G::kEnt * 16 + q * 16);
     const int64_t step_c = (int64_t)R.step * M.cstride, step_s = (int64_t)R.step * M.sstride;
+    const int whole = R.limit / R.step;  // tiles that are not cut short
     bool fresh = true;
     if (tid < 16) odd[tid] = 0;
     for (int b0 = t0; b0 < t1; b0 += s.batch) {
@@ -604,7 +609,7 @@ struct Product {
           if (++lb == hi) {
             lb = lo;
             ++lt;
-            if ((lt + 1) * (int64_t)R.step > R.limit) {
+            if (lt >= whole) {
               set_rows(M, R);  // the last tile may be cut short
             } else {
               pa += step_c; pb += step_c;
@@ -706,6 +711,294 @@ struct Product {
   }
 };
 
+// ---- one or two rows of x ---------------------------------------------------------------------------------
+// The same product for NTOK = 1 or 2 rows of x in the int8 form, with the activation operands in registers.
+// An MMA's 16 A rows are here 8 output rows x the two 32-byte halves of a 64-byte unit, and its 8 columns
+// the halves x the four digits; a half's rows only use its own columns (the others' results are dropped, the
+// tensor pipe has the time). So eight neighbouring lanes read 64 consecutive bytes of a row (half as many
+// lines a load as in Product), a warp keeps the operands of its C units of K in registers and runs down the
+// rows, and nothing but the codes and scales is loaded on the way: about 45 instructions per 512 bytes of
+// Q2, where Product has over 100 and shared-memory loads among them.
+// C: units (64 bytes) of a warp at most; D: tiles requested ahead.
+template <int L, int NTOK, int C, int D>
+struct Narrow {
+  using T = Lay<L>;
+  using G = Geo<L, kInt8>;
+  static constexpr int kRows = NTOK, kS = T::kSlots, kTiles = (NTOK + G::kTok - 1) / G::kTok;
+  static constexpr int kUnitBytes = 2 * kTiles * G::kTileBytes;  // operands of a 64-byte unit
+  static constexpr int kBlocksPerWarp = C;                       // for plan_split: a "block" is a 64-byte unit here
+  static constexpr int kTileRows = 8, kMode = kInt8;
+  static bool plan(int tiles, int units, size_t room, Split* out);
+
+  static __host__ __device__ size_t part_bytes(const Split& s) { return (size_t)s.batch * s.wk * 8 * kRows * 4; }
+  static __host__ __device__ size_t smem_bytes(const Split& s) {
+    return (size_t)s.pass * kUnitBytes + part_bytes(s) + kMaxWarps * 1024 + 64;
+  }
+
+  uint2 wa[D][C], wb[D][C];
+  uint32_t sa[D][C], sb[D][C];  // scales of the lane's half: one (Q2) or both slots
+  uint4 bop[C][NTOK][kS][G::kPairs];
+  int st[C][NTOK][kS][2];       // accumulator starts (binary: [0] is what twice the accumulators need added)
+  float sc[C][NTOK][kS];
+  const uint8_t *pa, *pb;
+  const uint16_t *ga, *gb;
+  int lt;
+
+  __device__ __forceinline__ void set_rows(const Mat& M, const Map& R, int ua) {
+    const int lane = threadIdx.x & 31, r = lane >> 3, h = (lane >> 2) & 1, q = lane & 3;
+    const int64_t o = (int64_t)lt * R.step + r;
+    const int64_t a = R.first + min(o, (int64_t)R.limit - 1), b = R.second + min(o + R.ahead, (int64_t)R.limit - 1);
+    pa = M.codes + a * M.cstride + 64 * ua + 32 * h + 8 * q;
+    pb = M.codes + b * M.cstride + 64 * ua + 32 * h + 8 * q;
+    ga = M.scales + a * M.sstride;
+    gb = M.scales + b * M.sstride;
+  }
+  // Tile at the cursor into ring slot d. in: bit c, whether the lane's bytes of unit c exist, bit 16 + c,
+  // whether its half of the unit does; g0, g1: groups.
+  __device__ __forceinline__ void request(int d, uint32_t in, const int (&g0)[C], const int (&g1)[C]) {
+#pragma unroll
+    for (int c = 0; c < C; c++) {
+      const bool on = in >> c & 1;
+      ldg_codes(wa[d][c], pa + 64 * c, on);
+      ldg_codes(wb[d][c], pb + 64 * c, on);
+      if (in >> (16 + c) & 1) {
+        if constexpr (kS == 1) {
+          sa[d][c] = __ldg(ga + g0[c]);
+          sb[d][c] = __ldg(gb + g0[c]);
+        } else {
+          sa[d][c] = __ldg(ga + g0[c]) | (uint32_t)__ldg(ga + g1[c]) << 16;
+          sb[d][c] = __ldg(gb + g0[c]) | (uint32_t)__ldg(gb + g1[c]) << 16;
+        }
+      }
+    }
+  }
+
+  // As Product::run: fin(tile, r, t, z, -) for tile row r of 8, or with R.ahead == 0 fin(tile, r, t, gate, up), r < 4.
+  template <class X, class First, class Fin>
+  __device__ __forceinline__ void run(uint8_t* smem, const Split& s, const Mat& M, const Map& R, int t0, int t1, const X& xs,
+                                      int tokens, First first, Fin fin) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = lane >> 2, q = lane & 3, h = g & 1;
+    uint8_t* frag = smem;
+    float* part = reinterpret_cast<float*>(smem + (size_t)s.pass * kUnitBytes);
+    uint32_t* scr = reinterpret_cast<uint32_t*>(smem + (size_t)s.pass * kUnitBytes + part_bytes(s)) + warp * 256;
+    int* odd = reinterpret_cast<int*>(smem + smem_bytes(s) - 64);
+    const int kg = warp % s.wk, tg = warp / s.wk;
+    const int units = (M.units + 1) / 2;  // of 64 bytes
+    const bool mine = (q >> 1) == h;      // this lane's columns belong to its rows' half
+    uint32_t k85 = 85u, kc80 = 0x00500050u;
+    asm volatile("" : "+r"(k85), "+r"(kc80));
+    const int64_t step_c = (int64_t)R.step * M.cstride, step_s = (int64_t)R.step * M.sstride;
+    const int whole = R.limit / R.step;  // tiles that are not cut short
+    bool fresh = true;
+    if (tid < 16) odd[tid] = 0;
+    for (int b0 = t0; b0 < t1; b0 += s.batch) {
+      const int b1 = min(t1, b0 + s.batch);
+      int ta = b0, tb = b0;
+      if (tg < s.tg) {
+        ta = b0 + (b1 - b0) * tg / s.tg;
+        tb = b0 + (b1 - b0) * (tg + 1) / s.tg;
+      }
+      for (int p0 = 0; p0 < units; p0 += s.pass) {
+        const int p1 = min(units, p0 + s.pass);
+        const int ua = p0 + (p1 - p0) * kg / s.wk, ub = p0 + (p1 - p0) * (kg + 1) / s.wk;
+        const int total = ua < ub ? tb - ta : 0;  // tiles
+        uint32_t in = 0;
+        int g0[C], g1[C];
+#pragma unroll
+        for (int c = 0; c < C; c++) {
+          const int v = 2 * (ua + c) + h;  // the lane's 32-byte unit
+          // (a lane past the end of a row's last half unit still holds results of that unit, and needs its scale)
+          if (ua + c < ub && 32 * v + 8 * q < M.row_bytes) in |= 1u << c;
+          if (ua + c < ub && v < M.units) in |= 1u << (16 + c);
+          const int gr = L == TERN_Q2_0_G128 ? v : (L == TERN_T3_5PB_G128 ? (5 * v) >> 2 : 2 * v);
+          g0[c] = min(gr, M.groups - 1);
+          g1[c] = min(gr + 1, M.groups - 1);  // (past the row's end its operands are zero)
+        }
+        int left = total;
+        lt = ta;
+        auto advance = [&]() {
+          --left;
+          ++lt;
+          if (lt >= whole) {
+            set_rows(M, R, ua);  // the last tile may be cut short
+          } else {
+            pa += step_c; pb += step_c;
+            ga += step_s; gb += step_s;
+          }
+        };
+        if (total > 0) set_rows(M, R, ua);
+#pragma unroll
+        for (int d = 0; d < D; d++) {
+#pragma unroll
+          for (int c = 0; c < C; c++) {
+            wa[d][c] = wb[d][c] = make_uint2(0, 0);
+            sa[d][c] = sb[d][c] = 0;
+          }
+          if (left > 0) {
+            request(d, in, g0, g1);
+            advance();
+          }
+        }
+        if (fresh) first();
+        if (fresh || s.pass < units) {
+          __syncthreads();  // the operands of the pass before have been taken (and the flags are clear)
+          const int v0 = 2 * p0, nv = min(M.units, 2 * p1) - v0;
+          for (uint32_t i = (uint32_t)nv * (kUnitBytes / 2) + tid * 16; i < (uint32_t)(2 * p1 - v0) * (kUnitBytes / 2); i += kThreads * 16)
+            *reinterpret_cast<uint4*>(frag + i) = make_uint4(0, 0, 0, 0);  // a half past the row's end
+          for (int i = warp; i < nv * NTOK; i += kMaxWarps) {
+            const int v = i / NTOK, t = i % NTOK;
+            if (t < tokens)
+              build_int8<L>(xs, t, t % G::kTok, v0 + v, M.K, scr,
+                            reinterpret_cast<uint4*>(frag + (size_t)v * (kUnitBytes / 2) + (t / G::kTok) * G::kTileBytes), odd + t);
+          }
+          __syncthreads();
+          // this lane's operands: column (half g / 4, digit g % 4), k by q; starts and scales of columns 2q, 2q + 1
+          const uint32_t base = sm100::smem_u32(frag);
+#pragma unroll
+          for (int c = 0; c < C; c++)
+#pragma unroll
+            for (int t = 0; t < NTOK; t++)
+#pragma unroll
+              for (int l = 0; l < kS; l++) {
+                const bool on = ua + c < ub && t < tokens;
+                const uint32_t tile = (uint32_t)((t / G::kTok) * G::kTileBytes);
+                const uint32_t ub_ = base + (uint32_t)(2 * (ua + c - p0) + (g >> 2)) * (kUnitBytes / 2) + tile;
+                const int ent = L == TERN_Q1_0_G128 ? q * 4 + (g & 3) : (L == TERN_Q2_0_G128 ? t : l) * 16 + q * 4 + (g & 3);
+#pragma unroll
+                for (int p = 0; p < G::kPairs; p++)
+                  bop[c][t][l][p] = lds128_if(ub_ + (uint32_t)((p * G::kEnt + ent) * 16), on && (L != TERN_Q1_0_G128 || l == (q >> 1)));
+                const uint32_t hd = base + (uint32_t)(2 * (ua + c - p0) + (q >> 1)) * (kUnitBytes / 2) + tile + G::kPairs * G::kEnt * 16;
+                const uint4 r = lds128_if(hd + (uint32_t)(((L == TERN_Q2_0_G128 ? t : l) * 2 + (q & 1)) * 16), on);
+                st[c][t][l][0] = (int)r.x;
+                st[c][t][l][1] = (int)r.y;
+                sc[c][t][l] = __uint_as_float(r.z);
+              }
+        }
+        fresh = false;
+        float* out = part + (size_t)((ta - b0) * s.wk + kg) * 8 * kRows;
+        for (int i = 0; i < total;) {
+#pragma unroll
+          for (int d = 0; d < D; d++) {
+            if (i >= total) break;
+            float acc[NTOK][2] = {};
+            uint2 xa[C], xb[C];
+            uint32_t ya[C], yb[C];
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+              xa[c] = wa[d][c]; xb[c] = wb[d][c];
+              ya[c] = sa[d][c]; yb[c] = sb[d][c];
+            }
+            if (left > 0) {
+              request(d, in, g0, g1);
+              advance();
+            }
+#pragma unroll
+            for (int c = 0; c < C; c++) {
+              uint32_t F[4][G::kPairs * 2];
+              operands8<L>(xa[c], xb[c], k85, kc80, F);
+#pragma unroll
+              for (int t = 0; t < NTOK; t++)
+#pragma unroll
+                for (int l = 0; l < kS; l++) {
+                  int e[4];
+                  e[0] = e[2] = L == TERN_Q1_0_G128 ? 0 : st[c][t][l][0];
+                  e[1] = e[3] = L == TERN_Q1_0_G128 ? 0 : st[c][t][l][1];
+#pragma unroll
+                  for (int p = 0; p < G::kPairs; p++) {
+                    const uint4& f = bop[c][t][l][p];
+                    mma_u8(e, F[0][2 * p], F[1][2 * p], F[2][2 * p], F[3][2 * p], f.x, f.y);
+                    if (2 * p + 1 < G::kMma) mma_u8(e, F[0][2 * p + 1], F[1][2 * p + 1], F[2][2 * p + 1], F[3][2 * p + 1], f.z, f.w);
+                  }
+                  int v0 = e[0] + 256 * e[1], v1 = e[2] + 256 * e[3];
+                  if (L == TERN_Q1_0_G128) {  // t = 2 b - 1
+                    v0 = 2 * v0 + st[c][t][l][0];
+                    v1 = 2 * v1 + st[c][t][l][0];
+                  }
+                  const float s0 = h2f((uint16_t)(l ? ya[c] >> 16 : ya[c] & 0xffffu)), s1 = h2f((uint16_t)(l ? yb[c] >> 16 : yb[c] & 0xffffu));
+                  acc[t][0] = fmaf(s0 * sc[c][t][l], (float)v0, acc[t][0]);
+                  acc[t][1] = fmaf(s1 * sc[c][t][l], (float)v1, acc[t][1]);
+                }
+            }
+            // a row's sums are in four lanes: digits 0-1 and 2-3 of the half in lanes 8 r, 8 r + 1, of the other
+            // half in lanes 8 r + 6, 8 r + 7; the lanes between hold other columns' results
+#pragma unroll
+            for (int t = 0; t < NTOK; t++) {
+              float v0 = mine ? acc[t][0] : 0.f, v1 = mine ? acc[t][1] : 0.f;
+              v0 += __shfl_xor_sync(0xffffffffu, v0, 1);
+              v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
+              v0 += __shfl_xor_sync(0xffffffffu, v0, 6);
+              v1 += __shfl_xor_sync(0xffffffffu, v1, 6);
+              if ((lane & 7) == 0) {
+                float *x = out + (lane >> 3) * kRows + t, *y = x + 4 * kRows;
+                *x = p0 > 0 ? *x + v0 : v0;
+                *y = p0 > 0 ? *y + v1 : v1;
+              }
+            }
+            out += s.wk * 8 * kRows;
+            i++;
+          }
+        }
+      }
+      __syncthreads();
+      const bool pairs = R.ahead == 0;
+      const int rows = pairs ? 4 : 8;
+      for (int i = tid; i < (b1 - b0) * rows * tokens; i += kThreads) {
+        const int r = i % rows, t = tokens == 1 ? 0 : (i / rows) % tokens, tl = i / (rows * tokens);
+        const int64_t o = (int64_t)(b0 + tl) * R.step + r;
+        if (o >= R.limit) continue;
+        const float* x = part + (size_t)tl * s.wk * 8 * kRows + r * kRows + t;
+        float z0 = 0.f, z1 = 0.f;
+#pragma unroll
+        for (int w = 0; w < kMaxWarps; w++)
+          if (w < s.wk) {
+            z0 += x[w * 8 * kRows];
+            if (pairs) z1 += x[(w * 8 + 4) * kRows];
+          }
+        if (odd[t]) {
+          const int64_t ra = R.first + o, rb = R.second + o;
+          for (int k = 0; k < M.K; k++) {
+            const float v = xs.at(t, k);
+            if (fabsf(v) <= 3.402823466e38f) continue;
+            z0 = fmaf(h2f(M.scales[ra * M.sstride + k / kGroup]) * decode_t(L, M.codes + ra * M.cstride, k), v, z0);
+            if (pairs) z1 = fmaf(h2f(M.scales[rb * M.sstride + k / kGroup]) * decode_t(L, M.codes + rb * M.cstride, k), v, z1);
+          }
+        }
+        fin(b0 + tl, r, t, z0, z1);
+      }
+      if (b1 < t1) __syncthreads();
+    }
+  }
+};
+
+// The cut for a Narrow product: wk warps along K with at most C units each, tg tile groups, so that the
+// busiest warp has the least to do; a tile's end counts as two thirds of a unit.
+template <class P>
+inline bool plan_narrow(int tiles, int units32, size_t room, Split* out) {
+  Split best{};
+  double best_cost = -1;
+  const int units = (units32 + 1) / 2;
+  for (int wk = std::min(units, kMaxWarps); wk >= 1; wk--) {
+    Split s{wk, std::max(1, std::min(kMaxWarps / wk, tiles)), 0, 0};
+    const size_t tile_bytes = (size_t)wk * 8 * P::kRows * 4, fixed = P::smem_bytes(Split{wk, 1, 0, 0});
+    s.batch = std::min<int>(tiles, std::max<int>(s.tg, (int)std::min<size_t>(room / 4 / tile_bytes, 256)));
+    const int most = (int)std::min<size_t>((size_t)wk * P::kBlocksPerWarp, (room - fixed - s.batch * tile_bytes) / P::kUnitBytes);
+    if (fixed + s.batch * tile_bytes > room || most < wk) continue;  // (the first pass gives every warp a unit)
+    const int passes = (units + most - 1) / most;
+    s.pass = std::max(wk, (units + passes - 1) / passes);
+    const int batches = (tiles + s.batch - 1) / s.batch;
+    const double per_group = (double)((s.batch + s.tg - 1) / s.tg);
+    const double work = per_group * ((s.pass + wk - 1) / wk + 0.67);
+    const double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * units : 0.0);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = s;
+    }
+  }
+  *out = best;
+  return best_cost >= 0;
+}
+
 // The cut for `tiles` tiles per CTA, `units` units of K and kRows rows of x within `room` bytes of shared
 // memory: as many blocks as fit beside the partial sums of a few tiles; then wk x tg warps so that the
 // busiest warp has the least to do, a tile's end counted as half a block. False when not even one block
@@ -738,6 +1031,20 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
   *out = best;
   return best_cost >= 0;
 }
+
+template <int L, int MODE, int NT>
+bool Product<L, MODE, NT>::plan(int tiles, int units, size_t room, Split* out) { return plan_split<Product>(tiles, units, room, out); }
+template <int L, int NTOK, int C, int D>
+bool Narrow<L, NTOK, C, D>::plan(int tiles, int units, size_t room, Split* out) { return plan_narrow<Narrow>(tiles, units, room, out); }
+
+// Units of a warp and tiles ahead that fit the registers.
+template <int L, int NTOK>
+#ifdef VC
+using NarrowFor = Narrow<L, NTOK, VC, VD>;
+#else
+using NarrowFor = Narrow<L, NTOK, L == TERN_Q2_0_G128 ? (NTOK == 1 ? 4 : 2) : L == TERN_T3_5PB_G128 && NTOK == 1 ? 2 : 1,
+                         L == TERN_Q2_0_G128 ? (NTOK == 1 ? 2 : 3) : L == TERN_T3_5PB_G128 && NTOK == 1 ? 2 : 4>;
+#endif
 
 }  // namespace rows
 }  // namespace tern
