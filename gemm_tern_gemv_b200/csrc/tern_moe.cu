@@ -50,9 +50,12 @@ __device__ __forceinline__ float exp_exact(double d) {
 
 // Logits in fp64 (products of fp16 values are exact in fp32), so that experts next to one another at the
 // border keep their order.
+// Where there are fewer experts than warps in a cluster, 2, 4 or 8 warps share an expert's dot product.
 template <int TOK>
 __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThreads) route_kernel(const __grid_constant__ MoeParams p) {
   __shared__ double logit[TOK][kMoeMaxExperts];
+  constexpr int kWarps = kRouteCtas * kRouteThreads / 32;
+  const int parts = p.experts * 8 <= kWarps ? 8 : p.experts * 4 <= kWarps ? 4 : p.experts * 2 <= kWarps ? 2 : 1;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t0 = (int)(blockIdx.x / kRouteCtas) * TOK;
   const int rank = (int)cluster_rank();
@@ -60,35 +63,44 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
   sm100::griddep_wait();
   for (int i = (int)(blockIdx.x * kRouteThreads + threadIdx.x); i < p.tokens * p.top_k + p.d / 8; i += (int)gridDim.x * kRouteThreads)
     p.clear[i] = 0;  // largest |h| of each pair, then the strips' counters
-  for (int e = rank + kRouteCtas * warp; e < p.experts; e += kRouteCtas * (kRouteThreads / 32)) {
+  for (int i = rank + kRouteCtas * warp; i < p.experts * parts; i += kWarps) {
+    const int e = i / parts, v0 = p.d / 8 * (i % parts) / parts, v1 = p.d / 8 * (i % parts + 1) / parts;
     double s[TOK][4] = {};  // four sums each: fp64 additions take long one after the other
     const uint4* w = reinterpret_cast<const uint4*>(p.router + (int64_t)e * p.d);
 #pragma unroll 4
-    for (int v = lane; v < p.d / 8; v += 32) {
+    for (int v = v0 + lane; v < v1; v += 32) {
       const uint4 a = __ldg(w + v);
       const uint32_t av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-      for (int i = 0; i < TOK; i++) {
-        if (t0 + i >= p.tokens) break;
-        const uint4 b = *(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + i) * p.d) + v);
+      for (int k = 0; k < TOK; k++) {
+        if (t0 + k >= p.tokens) break;
+        const uint4 b = *(reinterpret_cast<const uint4*>(p.x + (int64_t)(t0 + k) * p.d) + v);
         const uint32_t bv[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
         for (int q = 0; q < 4; q++) {
           const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&av[q])), y = __half22float2(*reinterpret_cast<const __half2*>(&bv[q]));
-          s[i][q] += (double)(x.x * y.x);
-          s[i][q] += (double)(x.y * y.y);
+          s[k][q] += (double)(x.x * y.x);
+          s[k][q] += (double)(x.y * y.y);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < TOK; i++) {
-      double v = (s[i][0] + s[i][1]) + (s[i][2] + s[i][3]);
+    for (int k = 0; k < TOK; k++) {
+      double v = (s[k][0] + s[k][1]) + (s[k][2] + s[k][3]);
       for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane == 0) store_first(&logit[i][e], v);
+      if (lane == 0) store_first(&logit[k][i], v);
     }
   }
   cluster_sync();
   if (rank || warp >= TOK || t0 + warp >= p.tokens) return;
+  if (parts > 1) {  // the parts' sums in their order; at most 64 of them, read before any is overwritten
+    double v = 0.;
+    if (lane < p.experts)
+      for (int i = 0; i < parts; i++) v += logit[warp][lane * parts + i];
+    __syncwarp();
+    if (lane < p.experts) logit[warp][lane] = v;
+    __syncwarp();
+  }
   // One warp per token; lane l holds the logits of experts l, l + 32, ... as 64-bit keys whose unsigned order
   // is the logits' (NaN last). Each pick is three warp reductions: high word, low word, lowest index.
   const int t = t0 + warp, per = (p.experts + 31) / 32;
@@ -158,6 +170,7 @@ struct Lists {
   uint32_t total[kMoeMaxExperts / 32];
   int index[16];                   // rows of the activations of the current segment
   float mul[16];                   // and their powers of two
+  uint32_t top[16];                // largest |h| of each in this CTA
   int last[kMaxStrips];            // strips that this CTA finished
 };
 
@@ -252,18 +265,22 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_up_kernel(const __grid_
   for (int t = (int)((int64_t)blockIdx.x * s.tiles / gridDim.x); t < t1;) {
     const int g = t / per, a = t % per, b = min(per, a + t1 - t), n = s.seg_count[g];
     const uint16_t* pair = s.pair + s.seg_first[g];
-    if ((int)threadIdx.x < n) s.index[threadIdx.x] = pair[threadIdx.x] / p.top_k;
+    if ((int)threadIdx.x < n) {
+      s.index[threadIdx.x] = pair[threadIdx.x] / p.top_k;
+      s.top[threadIdx.x] = 0;
+    }
     __syncthreads();
     const int64_t first = (int64_t)s.seg_expert[g] * 2 * p.f;
     P prod;
     prod.run(smem, split_for(q, b - a), q.mat, rows::Map{first, first + p.f, p.f, kStep, 0}, a, b, rows::HalfRows{p.x, p.d, s.index},
              n, [] {}, [&](int tile, int r, int c, float gate, float up) {
                const float h = act_fwd(p.act, gate) * up;
-               const int pr = pair[c];
-               p.h[(int64_t)pr * p.f + tile * kStep + r] = h;
+               p.h[(int64_t)pair[c] * p.f + tile * kStep + r] = h;
                // largest |h| of the pair, as bits: order does not matter to a maximum. NaN counts as the largest.
-               if (P::kMode == rows::kFp16) atomicMax(p.clear + pr, __float_as_uint(h) & 0x7fffffffu);
+               if (P::kMode == rows::kFp16) atomicMax(s.top + c, __float_as_uint(h) & 0x7fffffffu);
              });
+    __syncthreads();
+    if (P::kMode == rows::kFp16 && (int)threadIdx.x < n) atomicMax(p.clear + pair[threadIdx.x], s.top[threadIdx.x]);
     __syncthreads();
     t += b - a;
   }

@@ -1022,7 +1022,11 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
     const int batches = (tiles + s.batch - 1) / s.batch;
     const double per_group = (double)((s.batch + s.tg - 1) / s.tg);  // tiles of a tile group in a batch
     const double work = per_group * ((s.pass + wk - 1) / wk + 0.5);
-    const double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * blocks : 0.0);
+    double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * blocks : 0.0);
+    // warps side by side along K read a row's bytes together; far fewer than 1 KB of it at a time cost DRAM its
+    // open pages (16 warps on 16 tiles of their own: a third of the rate)
+    const int together = std::min(blocks, 8);
+    if (wk < together) cost *= 0.5 + 0.5 * together / wk;
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = s;
