@@ -1,9 +1,11 @@
 // The few-rows product core of the layer operators: y[t][o] = sum_k w[o][k] x[t][k] for a handful of
-// rows t of x, on mma.sync, weights read once from global memory straight into registers.
+// rows t of x, on mma.sync, weights read once from global memory.
 //
 // A row of packed codes is cut into units of 32 bytes (128 weights of Q2_0_g128, 160 of base-3, 256 of
 // binary); a warp takes 16 output rows and one unit at a time, each lane 8 bytes of rows g and g + 8
-// (g = lane / 4). A unit lies in one 128-weight group (Q2) or two (slots 0 and 1 of base-3 and binary).
+// (g = lane / 4). Four units, 128 bytes of a row, are a block: what a warp copies ahead into its own ring in
+// shared memory (cp.async, four whole lines an instruction; the copies need no registers and no barrier
+// but the warp's own). A unit lies in one 128-weight group (Q2) or two (slots 0 and 1 of base-3 and binary).
 // Two forms of the product:
 //   int8 (1-2 rows of x per tile of 8 MMA columns): activations become exact integers. Per unit, slot
 //     and row of x, X = round(x 2^S) with S from the largest |x| of the slot, written as four balanced
@@ -74,13 +76,24 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// 8 bytes of codes when pred is set (v keeps its value otherwise). Weights are read once: no place in L1.
-__device__ __forceinline__ void ldg_codes(uint2& v, const uint8_t* p, bool pred) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p ld.global.nc.L1::no_allocate.L2::256B.v2.u32 {%0,%1}, [%2];\n\t}"
-      : "+r"(v.x), "+r"(v.y)
-      : "l"(p), "r"((uint32_t)pred));
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
 }
+__device__ __forceinline__ uint32_t lds_u16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a));
+  return v;
+}
+// Copies of B bytes into shared memory; of `have` bytes at src only those are read, the rest arrives as zeros.
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, int have) {
+  if constexpr (B == 16) asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(have) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B), "r"(have) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Balanced base-256 digits of X (|X| <= 2^30): byte p of the result is d_p in [-128, 127], X = sum d_p 2^(8p).
 __device__ __forceinline__ uint32_t digits(int X) { return ((uint32_t)X + 0x00808080u) ^ 0x00808080u; }
@@ -304,8 +317,7 @@ struct Split {
   int wk, tg, pass, batch;
 };
 
-// A block is four units, 128 bytes of a row: what a warp requests and works off at a time. Its addresses
-// are one base and constant offsets, and a lane's scales of a row come in one or two loads.
+// A block is four units, 128 bytes of a row: what a warp copies and works off at a time.
 constexpr int kBlk = 4;
 
 // Code operands a0 .. a3 of each int8 MMA from 8 bytes of rows g (a) and g + 8 (b). k85, kc80: 85 and 80 in
@@ -351,84 +363,56 @@ struct Product {
   using T = Lay<L>;
   using G = Geo<L, MODE>;
   static constexpr int kRows = NT * G::kTok;             // rows of x
-  static constexpr int kDepth = 2;                       // blocks requested ahead by a warp
+  static constexpr int kDepth = MODE == kInt8 ? 3 : 2;   // blocks in a warp's ring
   static constexpr int kUnitBytes = NT * G::kTileBytes;  // activation operands of one unit
   static constexpr int kAcc = MODE == kInt8 ? 2 : 4;
   static constexpr int kTileRows = 16, kMode = MODE;
+  // scales of a block and row: Q2 four groups, binary eight; base-3 five, copied as the four words from the
+  // 4-byte boundary below the first on
+  static constexpr int kScaleBytes = L == TERN_Q2_0_G128 ? 8 : 16;
+  static constexpr int kStage = 16 * 128 + 16 * kScaleBytes;  // [16][128] codes, [16][kScaleBytes] scales
   static bool plan(int tiles, int units, size_t room, Split* out);
 
-  // shared memory: operands [pass], partial sums [batch][wk][16][kRows], scratch [warps][256 words], flags
+  // shared memory: operands [pass], partial sums [batch][wk][16][kRows], flags, scratch of the int8 operands'
+  // building, rings
   static __host__ __device__ size_t part_bytes(const Split& s) { return (size_t)s.batch * s.wk * 16 * kRows * 4; }
   static __host__ __device__ size_t smem_bytes(const Split& s) {
-    return (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s) + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 64;
+    return (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s) + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + kMaxWarps * kDepth * kStage + 64 + 128;
   }
 
-  uint2 wa[kDepth][kBlk], wb[kDepth][kBlk];
-  // group scales of the block's units: Q2 four groups; binary eight (the lane's slot picks); base-3 the
-  // lane's four
-  uint4 sa[kDepth], sb[kDepth];
-  // load cursor: codes (at the lane's bytes) and scales of the lane's two rows, tile, block
-  const uint8_t *pa, *pb;
-  const uint16_t *ga, *gb;
+  // copy cursor: this lane's four rows (lane / 8 + 4 i) of the tile's codes at its 16-byte piece of the block,
+  // and its row of scales; tile, block
+  const uint8_t* pc[4];
+  const uint16_t* ps;
   int lt, lb;
   uint32_t k85, kc80;  // opaque to the compiler, so that the base-3 steps stay multiplications
 
   __device__ __forceinline__ void set_rows(const Mat& M, const Map& R) {
-    const int g = (threadIdx.x & 31) >> 2, q = threadIdx.x & 3;
-    const int64_t o = (int64_t)lt * R.step + g;
-    const int64_t a = R.first + min(o, (int64_t)R.limit - 1), b = R.second + min(o + R.ahead, (int64_t)R.limit - 1);
-    pa = M.codes + a * M.cstride + 8 * q;
-    pb = M.codes + b * M.cstride + 8 * q;
-    ga = M.scales + a * M.sstride;
-    gb = M.scales + b * M.sstride;
-  }
-  __device__ __forceinline__ void request_scales(const Mat& M, int d) {
-    if constexpr (L == TERN_T3_5PB_G128) {  // a block of 640 weights starts at group 5 lb; unit j meets groups j, j + 1 of it
-      const int g0 = 5 * lb + ((threadIdx.x & 3) >> 1);
-      uint16_t u[4], v[4];
+    const int lane = threadIdx.x & 31;
+    const int64_t o = (int64_t)lt * R.step, last = (int64_t)R.limit - 1;
+    auto row = [&](int r) { return r < 8 ? R.first + min(o + r, last) : R.second + min(o + R.ahead + r - 8, last); };
 #pragma unroll
-      for (int j = 0; j < 4; j++) {
-        const int g = min(g0 + j, M.groups - 1);
-        u[j] = __ldg(ga + g);
-        v[j] = __ldg(gb + g);
-      }
-      sa[d] = make_uint4(u[0], u[1], u[2], u[3]);
-      sb[d] = make_uint4(v[0], v[1], v[2], v[3]);
-    } else {  // rows of scales are 16-byte aligned and a multiple of 16 bytes
-      constexpr int n = L == TERN_Q2_0_G128 ? 4 : 8;  // groups of a block
-      if constexpr (n == 4) {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(ga + 4 * lb)), v = __ldg(reinterpret_cast<const uint2*>(gb + 4 * lb));
-        sa[d] = make_uint4(u.x, u.y, 0, 0);
-        sb[d] = make_uint4(v.x, v.y, 0, 0);
-      } else {
-        sa[d] = __ldg(reinterpret_cast<const uint4*>(ga + 8 * lb));
-        sb[d] = __ldg(reinterpret_cast<const uint4*>(gb + 8 * lb));
-      }
-      const int have = M.groups - n * lb;
-      if (have < n) {  // what lies past the row's last group counts as 0
-        auto keep = [&](uint32_t w, int i) { return 2 * i >= have ? 0u : (2 * i + 1 >= have ? w & 0xffffu : w); };
-        sa[d] = make_uint4(keep(sa[d].x, 0), keep(sa[d].y, 1), keep(sa[d].z, 2), keep(sa[d].w, 3));
-        sb[d] = make_uint4(keep(sb[d].x, 0), keep(sb[d].y, 1), keep(sb[d].z, 2), keep(sb[d].w, 3));
-      }
-    }
+    for (int i = 0; i < 4; i++) pc[i] = M.codes + row((lane >> 3) + 4 * i) * M.cstride + 16 * (lane & 7);
+    ps = M.scales + row(L == TERN_T3_5PB_G128 ? lane >> 1 : lane & 15) * M.sstride;
   }
-  // Unit j of the block at the cursor. The row may end inside the block (a base-3 or binary row inside a
-  // unit): what lies past it is not read, its operands are zero and any codes will do.
-  __device__ __forceinline__ void request_unit(const Mat& M, int d, int j, bool on) {
-    const int off = lb * 128 + j * 32;
-    const bool in = on && off + 8 * (int)(threadIdx.x & 3) < M.row_bytes;
-    ldg_codes(wa[d][j], pa + off, in);
-    ldg_codes(wb[d][j], pb + off, in);
-  }
-  __device__ __forceinline__ float scale(const uint4& s, int j) const {
-    if constexpr (L == TERN_Q2_0_G128) {
-      const uint32_t w = j < 2 ? s.x : s.y;
-      return h2f((uint16_t)((j & 1) ? w >> 16 : w & 0xffffu));
-    } else if constexpr (L == TERN_Q1_0_G128) {
-      const uint32_t w = j == 0 ? s.x : (j == 1 ? s.y : (j == 2 ? s.z : s.w));
-      return h2f((uint16_t)((threadIdx.x & 2) ? w >> 16 : w & 0xffffu));
+  // The block at the cursor into the ring stage at `stage`. Piece c of a row lies at (c / 2 ^ row % 4) * 32 +
+  // c % 2 * 16, so that the four rows a half-warp reads 32 bytes of are in different banks.
+  __device__ __forceinline__ void request(const Mat& M, uint32_t stage) {
+    const int lane = threadIdx.x & 31, c = lane & 7;
+    const int off = lb * 128, have = min(max(M.row_bytes - off - 16 * c, 0), 16);
+    const uint32_t dst = stage + (lane >> 3) * 128 + (((c >> 1) ^ (lane >> 3)) * 32) + (c & 1) * 16;
+#pragma unroll
+    for (int i = 0; i < 4; i++) copy_async<16>(dst + i * 512, pc[i] + off, have);
+    const uint32_t ds = stage + 16 * 128;
+    if constexpr (L == TERN_T3_5PB_G128) {
+      // groups 5 lb .. 5 lb + 4 of a row, two words a lane
+      const int w = ((10 * lb) & ~3) + 8 * (lane & 1), left = 2 * M.groups - w;
+#pragma unroll
+      for (int i = 0; i < 2; i++)
+        copy_async<4>(ds + (lane >> 1) * 16 + 8 * (lane & 1) + 4 * i, reinterpret_cast<const uint8_t*>(ps) + w + 4 * i, min(max(left - 4 * i, 0), 4));
     } else {
-      return h2f((uint16_t)(j == 0 ? s.x : (j == 1 ? s.y : (j == 2 ? s.z : s.w))));
+      const int left = 2 * M.groups - kScaleBytes * lb;
+      if (lane < 16) copy_async<kScaleBytes>(ds + lane * kScaleBytes, reinterpret_cast<const uint8_t*>(ps) + kScaleBytes * lb, min(max(left, 0), kScaleBytes));
     }
   }
 
@@ -559,8 +543,10 @@ struct Product {
     const int g = lane >> 2, q = lane & 3;
     uint8_t* frag = smem;
     float* part = reinterpret_cast<float*>(smem + (size_t)s.pass * kBlk * kUnitBytes);
-    uint32_t* scr = reinterpret_cast<uint32_t*>(smem + (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s)) + warp * 256;
-    int* odd = reinterpret_cast<int*>(smem + smem_bytes(s) - 64);  // rows of x with a non-finite activation
+    uint8_t* tail = smem + (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s);
+    int* odd = reinterpret_cast<int*>(tail);  // rows of x with a non-finite activation
+    uint32_t* scr = reinterpret_cast<uint32_t*>(tail + 64) + warp * 256;
+    const uint32_t ring = ((sm100::smem_u32(tail) + 64 + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 127) & ~127u) + warp * (kDepth * kStage);
     const int kg = warp % s.wk, tg = warp / s.wk;
     const int blocks = (M.units + kBlk - 1) / kBlk;
     k85 = 85u;
@@ -587,6 +573,7 @@ struct Product {
     const uint32_t hd0 = base0 + (uint32_t)(G::kPairs * G::kEnt * 16 + q * 16);
     const int64_t step_c = (int64_t)R.step * M.cstride, step_s = (int64_t)R.step * M.sstride;
     const int whole = R.limit / R.step;  // tiles that are not cut short
+    const uint32_t lane_c = (uint32_t)(g * 128 + (g & 3) * 32 + 8 * q);  // unit 0 of row g in a stage
     bool fresh = true;
     if (tid < 16) odd[tid] = 0;
     for (int b0 = t0; b0 < t1; b0 += s.batch) {
@@ -599,35 +586,31 @@ struct Product {
       for (int p0 = 0; p0 < blocks; p0 += s.pass) {
         const int p1 = min(blocks, p0 + s.pass);
         const int lo = p0 + (p1 - p0) * kg / s.wk, hi = p0 + (p1 - p0) * (kg + 1) / s.wk;  // the warp's blocks
-        int left = (tb - ta) * (hi - lo);  // blocks still to be requested
+        int left = (tb - ta) * (hi - lo);  // blocks still to be copied
+        const int total = left;
         lt = ta;
         lb = lo;
-        const int total = left;
-        if (left > 0) set_rows(M, R);
-        auto advance = [&]() {
-          --left;
-          if (++lb == hi) {
-            lb = lo;
-            ++lt;
-            if (lt >= whole) {
-              set_rows(M, R);  // the last tile may be cut short
-            } else {
-              pa += step_c; pb += step_c;
-              ga += step_s; gb += step_s;
-            }
-          }
-        };
-#pragma unroll
-        for (int d = 0; d < kDepth; d++)
+        auto next = [&](uint32_t stage) {  // requests a block, or nothing; one group of copies either way
           if (left > 0) {
-            request_scales(M, d);
+            request(M, stage);
+            --left;
+            if (++lb == hi) {
+              lb = lo;
+              ++lt;
+              if (lt >= whole) {
+                set_rows(M, R);  // the last tile may be cut short
+              } else {
 #pragma unroll
-            for (int j = 0; j < kBlk; j++) {
-              wa[d][j] = wb[d][j] = make_uint2(0, 0);
-              request_unit(M, d, j, true);
+                for (int i = 0; i < 4; i++) pc[i] += step_c;
+                ps += step_s;
+              }
             }
-            advance();
           }
+          copy_commit();
+        };
+        if (left > 0) set_rows(M, R);
+#pragma unroll 1
+        for (int d = 0; d < kDepth; d++) next(ring + d * kStage);
         if (fresh) first();
         if (fresh || s.pass < blocks) {
           __syncthreads();  // the operands of the pass before are no longer read (and the flags are clear)
@@ -635,57 +618,73 @@ struct Product {
           for (uint32_t i = (uint32_t)nu * kUnitBytes + tid * 16; i < (uint32_t)(p1 * kBlk - u0) * kUnitBytes; i += kThreads * 16)
             *reinterpret_cast<uint4*>(frag + i) = make_uint4(0, 0, 0, 0);  // units past the row's end
           if constexpr (MODE == kInt8) {
-            for (int i = warp; i < nu * tokens; i += kMaxWarps) {
-              const int u = i / tokens, t = i % tokens;
-              build_int8<L>(xs, t, t % G::kTok, u0 + u, M.K, scr,
-                            reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes), odd + t);
-            }
+#pragma unroll 1
+            for (int t = 0; t < tokens; t++)
+#pragma unroll 1
+              for (int u = warp; u < nu; u += kMaxWarps)
+                build_int8<L>(xs, t, t % G::kTok, u0 + u, M.K, scr,
+                              reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes), odd + t);
           } else {
-            for (int i = warp; i < nu * NT; i += kMaxWarps) {
-              const int u = i / NT, n = i % NT;
-              build_fp16<L>(xs, n * G::kTok, tokens, u0 + u, M.K,
-                            reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + n * G::kTileBytes));
-            }
+#pragma unroll 1
+            for (int n = 0; n < NT; n++)
+#pragma unroll 1
+              for (int u = warp; u < nu; u += kMaxWarps)
+                build_fp16<L>(xs, n * G::kTok, tokens, u0 + u, M.K,
+                              reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + n * G::kTileBytes));
           }
           __syncthreads();
         }
         fresh = false;
-        if (total > 0) {
-          float acc[NT][kAcc] = {};
-          int cb = lo;
-          float* out = part + (size_t)((ta - b0) * s.wk + kg) * 16 * kRows;
-          for (int i = total; i > 0;) {
+        float acc[NT][kAcc] = {};
+        int cb = lo;
+        uint32_t stage = ring;
+        float* out = part + (size_t)((ta - b0) * s.wk + kg) * 16 * kRows;
+#pragma unroll 1
+        for (int i = 0; i < total; i++) {
+          copy_wait<kDepth - 1>();
+          __syncwarp();
+          const uint32_t fo = (uint32_t)((cb - p0) * kBlk * kUnitBytes);
+          uint32_t sa[kBlk], sb[kBlk];  // scales of rows g and g + 8, as fp16 bits
+          const uint32_t sc = stage + 16 * 128 + g * kScaleBytes;
+          if constexpr (L == TERN_Q2_0_G128) {
+            const uint2 a = lds64(sc), b = lds64(sc + 8 * kScaleBytes);
+            sa[0] = a.x & 0xffff; sa[1] = a.x >> 16; sa[2] = a.y & 0xffff; sa[3] = a.y >> 16;
+            sb[0] = b.x & 0xffff; sb[1] = b.x >> 16; sb[2] = b.y & 0xffff; sb[3] = b.y >> 16;
+          } else {
+            const uint32_t at = sc + (L == TERN_Q1_0_G128 ? (q & 2) : ((10 * cb) & 3) + (q & 2));  // by the lane's slot
 #pragma unroll
-            for (int d = 0; d < kDepth; d++) {
-              if (i <= 0) break;
-              const uint4 s0 = sa[d], s1 = sb[d];
-              const bool ml = left > 0;
-              if (ml) request_scales(M, d);
-              const uint32_t fo = (uint32_t)((cb - p0) * kBlk * kUnitBytes);
-#pragma unroll
-              for (int j = 0; j < kBlk; j++) {
-                const uint2 a = wa[d][j], b = wb[d][j];
-                request_unit(M, d, j, ml);
-                unit(a, b, scale(s0, j), scale(s1, j), base0 + fo + j * kUnitBytes, hd0 + fo + j * kUnitBytes, ent, acc);
-              }
-              if (ml) advance();
-              --i;
-              if (++cb == hi) {
-                store_part(out, p0 > 0, acc);
-                cb = lo;
-                out += s.wk * 16 * kRows;
-              }
+            for (int j = 0; j < kBlk; j++) {
+              sa[j] = lds_u16(at + (L == TERN_Q1_0_G128 ? 4 : 2) * j);
+              sb[j] = lds_u16(at + (L == TERN_Q1_0_G128 ? 4 : 2) * j + 8 * kScaleBytes);
             }
           }
+          uint2 a[kBlk], b[kBlk];
+#pragma unroll
+          for (int j = 0; j < kBlk; j++) {
+            const uint32_t at = (stage + lane_c) ^ (32u * j);
+            a[j] = lds64(at);
+            b[j] = lds64(at + 8 * 128);
+          }
+          __syncwarp();  // every lane has read the stage
+          next(stage);
+          stage = stage == ring + (kDepth - 1) * kStage ? ring : stage + kStage;
+#pragma unroll
+          for (int j = 0; j < kBlk; j++)
+            unit(a[j], b[j], h2f((uint16_t)sa[j]), h2f((uint16_t)sb[j]), base0 + fo + j * kUnitBytes, hd0 + fo + j * kUnitBytes, ent, acc);
+          if (++cb == hi) {
+            store_part(out, p0 > 0, acc);
+            cb = lo;
+            out += s.wk * 16 * kRows;
+          }
         }
+        copy_wait<0>();
       }
       __syncthreads();
       // the wk partial sums of each output, in order
       const bool pairs = R.ahead == 0;
-      const int rows = pairs ? 8 : 16;
-      const int outs = (b1 - b0) * rows * tokens;
-      for (int i = tid; i < outs; i += kThreads) {
-        const int r = i % rows, t = (i / rows) % tokens, tl = i / (rows * tokens);
+      const int rows = pairs ? 8 : 16, shift = pairs ? 3 : 4;
+      for (int i = tid; i < (b1 - b0) * rows * tokens; i += kThreads) {
+        const int r = i & (rows - 1), tt = i >> shift, t = tokens == 1 ? 0 : tt % tokens, tl = tokens == 1 ? tt : tt / tokens;
         const int64_t o = (int64_t)(b0 + tl) * R.step + r;
         if (o >= R.limit) continue;
         const float* x = part + (size_t)tl * s.wk * 16 * kRows + r * kRows + t;
@@ -710,294 +709,6 @@ struct Product {
     }
   }
 };
-
-// ---- one or two rows of x ---------------------------------------------------------------------------------
-// The same product for NTOK = 1 or 2 rows of x in the int8 form, with the activation operands in registers.
-// An MMA's 16 A rows are here 8 output rows x the two 32-byte halves of a 64-byte unit, and its 8 columns
-// the halves x the four digits; a half's rows only use its own columns (the others' results are dropped, the
-// tensor pipe has the time). So eight neighbouring lanes read 64 consecutive bytes of a row (half as many
-// lines a load as in Product), a warp keeps the operands of its C units of K in registers and runs down the
-// rows, and nothing but the codes and scales is loaded on the way: about 45 instructions per 512 bytes of
-// Q2, where Product has over 100 and shared-memory loads among them.
-// C: units (64 bytes) of a warp at most; D: tiles requested ahead.
-template <int L, int NTOK, int C, int D>
-struct Narrow {
-  using T = Lay<L>;
-  using G = Geo<L, kInt8>;
-  static constexpr int kRows = NTOK, kS = T::kSlots, kTiles = (NTOK + G::kTok - 1) / G::kTok;
-  static constexpr int kUnitBytes = 2 * kTiles * G::kTileBytes;  // operands of a 64-byte unit
-  static constexpr int kBlocksPerWarp = C;                       // for plan_split: a "block" is a 64-byte unit here
-  static constexpr int kTileRows = 8, kMode = kInt8;
-  static bool plan(int tiles, int units, size_t room, Split* out);
-
-  static __host__ __device__ size_t part_bytes(const Split& s) { return (size_t)s.batch * s.wk * 8 * kRows * 4; }
-  static __host__ __device__ size_t smem_bytes(const Split& s) {
-    return (size_t)s.pass * kUnitBytes + part_bytes(s) + kMaxWarps * 1024 + 64;
-  }
-
-  uint2 wa[D][C], wb[D][C];
-  uint32_t sa[D][C], sb[D][C];  // scales of the lane's half: one (Q2) or both slots
-  uint4 bop[C][NTOK][kS][G::kPairs];
-  int st[C][NTOK][kS][2];       // accumulator starts (binary: [0] is what twice the accumulators need added)
-  float sc[C][NTOK][kS];
-  const uint8_t *pa, *pb;
-  const uint16_t *ga, *gb;
-  int lt;
-
-  __device__ __forceinline__ void set_rows(const Mat& M, const Map& R, int ua) {
-    const int lane = threadIdx.x & 31, r = lane >> 3, h = (lane >> 2) & 1, q = lane & 3;
-    const int64_t o = (int64_t)lt * R.step + r;
-    const int64_t a = R.first + min(o, (int64_t)R.limit - 1), b = R.second + min(o + R.ahead, (int64_t)R.limit - 1);
-    pa = M.codes + a * M.cstride + 64 * ua + 32 * h + 8 * q;
-    pb = M.codes + b * M.cstride + 64 * ua + 32 * h + 8 * q;
-    ga = M.scales + a * M.sstride;
-    gb = M.scales + b * M.sstride;
-  }
-  // Tile at the cursor into ring slot d. in: bit c, whether the lane's bytes of unit c exist, bit 16 + c,
-  // whether its half of the unit does; g0, g1: groups.
-  __device__ __forceinline__ void request(int d, uint32_t in, const int (&g0)[C], const int (&g1)[C]) {
-#pragma unroll
-    for (int c = 0; c < C; c++) {
-      const bool on = in >> c & 1;
-      ldg_codes(wa[d][c], pa + 64 * c, on);
-      ldg_codes(wb[d][c], pb + 64 * c, on);
-      if (in >> (16 + c) & 1) {
-        if constexpr (kS == 1) {
-          sa[d][c] = __ldg(ga + g0[c]);
-          sb[d][c] = __ldg(gb + g0[c]);
-        } else {
-          sa[d][c] = __ldg(ga + g0[c]) | (uint32_t)__ldg(ga + g1[c]) << 16;
-          sb[d][c] = __ldg(gb + g0[c]) | (uint32_t)__ldg(gb + g1[c]) << 16;
-        }
-      }
-    }
-  }
-
-  // As Product::run: fin(tile, r, t, z, -) for tile row r of 8, or with R.ahead == 0 fin(tile, r, t, gate, up), r < 4.
-  template <class X, class First, class Fin>
-  __device__ __forceinline__ void run(uint8_t* smem, const Split& s, const Mat& M, const Map& R, int t0, int t1, const X& xs,
-                                      int tokens, First first, Fin fin) {
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int g = lane >> 2, q = lane & 3, h = g & 1;
-    uint8_t* frag = smem;
-    float* part = reinterpret_cast<float*>(smem + (size_t)s.pass * kUnitBytes);
-    uint32_t* scr = reinterpret_cast<uint32_t*>(smem + (size_t)s.pass * kUnitBytes + part_bytes(s)) + warp * 256;
-    int* odd = reinterpret_cast<int*>(smem + smem_bytes(s) - 64);
-    const int kg = warp % s.wk, tg = warp / s.wk;
-    const int units = (M.units + 1) / 2;  // of 64 bytes
-    const bool mine = (q >> 1) == h;      // this lane's columns belong to its rows' half
-    uint32_t k85 = 85u, kc80 = 0x00500050u;
-    asm volatile("" : "+r"(k85), "+r"(kc80));
-    const int64_t step_c = (int64_t)R.step * M.cstride, step_s = (int64_t)R.step * M.sstride;
-    const int whole = R.limit / R.step;  // tiles that are not cut short
-    bool fresh = true;
-    if (tid < 16) odd[tid] = 0;
-    for (int b0 = t0; b0 < t1; b0 += s.batch) {
-      const int b1 = min(t1, b0 + s.batch);
-      int ta = b0, tb = b0;
-      if (tg < s.tg) {
-        ta = b0 + (b1 - b0) * tg / s.tg;
-        tb = b0 + (b1 - b0) * (tg + 1) / s.tg;
-      }
-      for (int p0 = 0; p0 < units; p0 += s.pass) {
-        const int p1 = min(units, p0 + s.pass);
-        const int ua = p0 + (p1 - p0) * kg / s.wk, ub = p0 + (p1 - p0) * (kg + 1) / s.wk;
-        const int total = ua < ub ? tb - ta : 0;  // tiles
-        uint32_t in = 0;
-        int g0[C], g1[C];
-#pragma unroll
-        for (int c = 0; c < C; c++) {
-          const int v = 2 * (ua + c) + h;  // the lane's 32-byte unit
-          // (a lane past the end of a row's last half unit still holds results of that unit, and needs its scale)
-          if (ua + c < ub && 32 * v + 8 * q < M.row_bytes) in |= 1u << c;
-          if (ua + c < ub && v < M.units) in |= 1u << (16 + c);
-          const int gr = L == TERN_Q2_0_G128 ? v : (L == TERN_T3_5PB_G128 ? (5 * v) >> 2 : 2 * v);
-          g0[c] = min(gr, M.groups - 1);
-          g1[c] = min(gr + 1, M.groups - 1);  // (past the row's end its operands are zero)
-        }
-        int left = total;
-        lt = ta;
-        auto advance = [&]() {
-          --left;
-          ++lt;
-          if (lt >= whole) {
-            set_rows(M, R, ua);  // the last tile may be cut short
-          } else {
-            pa += step_c; pb += step_c;
-            ga += step_s; gb += step_s;
-          }
-        };
-        if (total > 0) set_rows(M, R, ua);
-#pragma unroll
-        for (int d = 0; d < D; d++) {
-#pragma unroll
-          for (int c = 0; c < C; c++) {
-            wa[d][c] = wb[d][c] = make_uint2(0, 0);
-            sa[d][c] = sb[d][c] = 0;
-          }
-          if (left > 0) {
-            request(d, in, g0, g1);
-            advance();
-          }
-        }
-        if (fresh) first();
-        if (fresh || s.pass < units) {
-          __syncthreads();  // the operands of the pass before have been taken (and the flags are clear)
-          const int v0 = 2 * p0, nv = min(M.units, 2 * p1) - v0;
-          for (uint32_t i = (uint32_t)nv * (kUnitBytes / 2) + tid * 16; i < (uint32_t)(2 * p1 - v0) * (kUnitBytes / 2); i += kThreads * 16)
-            *reinterpret_cast<uint4*>(frag + i) = make_uint4(0, 0, 0, 0);  // a half past the row's end
-          for (int i = warp; i < nv * NTOK; i += kMaxWarps) {
-            const int v = i / NTOK, t = i % NTOK;
-            if (t < tokens)
-              build_int8<L>(xs, t, t % G::kTok, v0 + v, M.K, scr,
-                            reinterpret_cast<uint4*>(frag + (size_t)v * (kUnitBytes / 2) + (t / G::kTok) * G::kTileBytes), odd + t);
-          }
-          __syncthreads();
-          // this lane's operands: column (half g / 4, digit g % 4), k by q; starts and scales of columns 2q, 2q + 1
-          const uint32_t base = sm100::smem_u32(frag);
-#pragma unroll
-          for (int c = 0; c < C; c++)
-#pragma unroll
-            for (int t = 0; t < NTOK; t++)
-#pragma unroll
-              for (int l = 0; l < kS; l++) {
-                const bool on = ua + c < ub && t < tokens;
-                const uint32_t tile = (uint32_t)((t / G::kTok) * G::kTileBytes);
-                const uint32_t ub_ = base + (uint32_t)(2 * (ua + c - p0) + (g >> 2)) * (kUnitBytes / 2) + tile;
-                const int ent = L == TERN_Q1_0_G128 ? q * 4 + (g & 3) : (L == TERN_Q2_0_G128 ? t : l) * 16 + q * 4 + (g & 3);
-#pragma unroll
-                for (int p = 0; p < G::kPairs; p++)
-                  bop[c][t][l][p] = lds128_if(ub_ + (uint32_t)((p * G::kEnt + ent) * 16), on && (L != TERN_Q1_0_G128 || l == (q >> 1)));
-                const uint32_t hd = base + (uint32_t)(2 * (ua + c - p0) + (q >> 1)) * (kUnitBytes / 2) + tile + G::kPairs * G::kEnt * 16;
-                const uint4 r = lds128_if(hd + (uint32_t)(((L == TERN_Q2_0_G128 ? t : l) * 2 + (q & 1)) * 16), on);
-                st[c][t][l][0] = (int)r.x;
-                st[c][t][l][1] = (int)r.y;
-                sc[c][t][l] = __uint_as_float(r.z);
-              }
-        }
-        fresh = false;
-        float* out = part + (size_t)((ta - b0) * s.wk + kg) * 8 * kRows;
-        for (int i = 0; i < total;) {
-#pragma unroll
-          for (int d = 0; d < D; d++) {
-            if (i >= total) break;
-            float acc[NTOK][2] = {};
-            uint2 xa[C], xb[C];
-            uint32_t ya[C], yb[C];
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-              xa[c] = wa[d][c]; xb[c] = wb[d][c];
-              ya[c] = sa[d][c]; yb[c] = sb[d][c];
-            }
-            if (left > 0) {
-              request(d, in, g0, g1);
-              advance();
-            }
-#pragma unroll
-            for (int c = 0; c < C; c++) {
-              uint32_t F[4][G::kPairs * 2];
-              operands8<L>(xa[c], xb[c], k85, kc80, F);
-#pragma unroll
-              for (int t = 0; t < NTOK; t++)
-#pragma unroll
-                for (int l = 0; l < kS; l++) {
-                  int e[4];
-                  e[0] = e[2] = L == TERN_Q1_0_G128 ? 0 : st[c][t][l][0];
-                  e[1] = e[3] = L == TERN_Q1_0_G128 ? 0 : st[c][t][l][1];
-#pragma unroll
-                  for (int p = 0; p < G::kPairs; p++) {
-                    const uint4& f = bop[c][t][l][p];
-                    mma_u8(e, F[0][2 * p], F[1][2 * p], F[2][2 * p], F[3][2 * p], f.x, f.y);
-                    if (2 * p + 1 < G::kMma) mma_u8(e, F[0][2 * p + 1], F[1][2 * p + 1], F[2][2 * p + 1], F[3][2 * p + 1], f.z, f.w);
-                  }
-                  int v0 = e[0] + 256 * e[1], v1 = e[2] + 256 * e[3];
-                  if (L == TERN_Q1_0_G128) {  // t = 2 b - 1
-                    v0 = 2 * v0 + st[c][t][l][0];
-                    v1 = 2 * v1 + st[c][t][l][0];
-                  }
-                  const float s0 = h2f((uint16_t)(l ? ya[c] >> 16 : ya[c] & 0xffffu)), s1 = h2f((uint16_t)(l ? yb[c] >> 16 : yb[c] & 0xffffu));
-                  acc[t][0] = fmaf(s0 * sc[c][t][l], (float)v0, acc[t][0]);
-                  acc[t][1] = fmaf(s1 * sc[c][t][l], (float)v1, acc[t][1]);
-                }
-            }
-            // a row's sums are in four lanes: digits 0-1 and 2-3 of the half in lanes 8 r, 8 r + 1, of the other
-            // half in lanes 8 r + 6, 8 r + 7; the lanes between hold other columns' results
-#pragma unroll
-            for (int t = 0; t < NTOK; t++) {
-              float v0 = mine ? acc[t][0] : 0.f, v1 = mine ? acc[t][1] : 0.f;
-              v0 += __shfl_xor_sync(0xffffffffu, v0, 1);
-              v1 += __shfl_xor_sync(0xffffffffu, v1, 1);
-              v0 += __shfl_xor_sync(0xffffffffu, v0, 6);
-              v1 += __shfl_xor_sync(0xffffffffu, v1, 6);
-              if ((lane & 7) == 0) {
-                float *x = out + (lane >> 3) * kRows + t, *y = x + 4 * kRows;
-                *x = p0 > 0 ? *x + v0 : v0;
-                *y = p0 > 0 ? *y + v1 : v1;
-              }
-            }
-            out += s.wk * 8 * kRows;
-            i++;
-          }
-        }
-      }
-      __syncthreads();
-      const bool pairs = R.ahead == 0;
-      const int rows = pairs ? 4 : 8;
-      for (int i = tid; i < (b1 - b0) * rows * tokens; i += kThreads) {
-        const int r = i % rows, t = tokens == 1 ? 0 : (i / rows) % tokens, tl = i / (rows * tokens);
-        const int64_t o = (int64_t)(b0 + tl) * R.step + r;
-        if (o >= R.limit) continue;
-        const float* x = part + (size_t)tl * s.wk * 8 * kRows + r * kRows + t;
-        float z0 = 0.f, z1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < kMaxWarps; w++)
-          if (w < s.wk) {
-            z0 += x[w * 8 * kRows];
-            if (pairs) z1 += x[(w * 8 + 4) * kRows];
-          }
-        if (odd[t]) {
-          const int64_t ra = R.first + o, rb = R.second + o;
-          for (int k = 0; k < M.K; k++) {
-            const float v = xs.at(t, k);
-            if (fabsf(v) <= 3.402823466e38f) continue;
-            z0 = fmaf(h2f(M.scales[ra * M.sstride + k / kGroup]) * decode_t(L, M.codes + ra * M.cstride, k), v, z0);
-            if (pairs) z1 = fmaf(h2f(M.scales[rb * M.sstride + k / kGroup]) * decode_t(L, M.codes + rb * M.cstride, k), v, z1);
-          }
-        }
-        fin(b0 + tl, r, t, z0, z1);
-      }
-      if (b1 < t1) __syncthreads();
-    }
-  }
-};
-
-// The cut for a Narrow product: wk warps along K with at most C units each, tg tile groups, so that the
-// busiest warp has the least to do; a tile's end counts as two thirds of a unit.
-template <class P>
-inline bool plan_narrow(int tiles, int units32, size_t room, Split* out) {
-  Split best{};
-  double best_cost = -1;
-  const int units = (units32 + 1) / 2;
-  for (int wk = std::min(units, kMaxWarps); wk >= 1; wk--) {
-    Split s{wk, std::max(1, std::min(kMaxWarps / wk, tiles)), 0, 0};
-    const size_t tile_bytes = (size_t)wk * 8 * P::kRows * 4, fixed = P::smem_bytes(Split{wk, 1, 0, 0});
-    s.batch = std::min<int>(tiles, std::max<int>(s.tg, (int)std::min<size_t>(room / 4 / tile_bytes, 256)));
-    const int most = (int)std::min<size_t>((size_t)wk * P::kBlocksPerWarp, (room - fixed - s.batch * tile_bytes) / P::kUnitBytes);
-    if (fixed + s.batch * tile_bytes > room || most < wk) continue;  // (the first pass gives every warp a unit)
-    const int passes = (units + most - 1) / most;
-    s.pass = std::max(wk, (units + passes - 1) / passes);
-    const int batches = (tiles + s.batch - 1) / s.batch;
-    const double per_group = (double)((s.batch + s.tg - 1) / s.tg);
-    const double work = per_group * ((s.pass + wk - 1) / wk + 0.67);
-    const double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * units : 0.0);
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = s;
-    }
-  }
-  *out = best;
-  return best_cost >= 0;
-}
 
 // The cut for `tiles` tiles per CTA, `units` units of K and kRows rows of x within `room` bytes of shared
 // memory: as many blocks as fit beside the partial sums of a few tiles; then wk x tg warps so that the
@@ -1038,17 +749,6 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
 
 template <int L, int MODE, int NT>
 bool Product<L, MODE, NT>::plan(int tiles, int units, size_t room, Split* out) { return plan_split<Product>(tiles, units, room, out); }
-template <int L, int NTOK, int C, int D>
-bool Narrow<L, NTOK, C, D>::plan(int tiles, int units, size_t room, Split* out) { return plan_narrow<Narrow>(tiles, units, room, out); }
-
-// Units of a warp and tiles ahead that fit the registers.
-template <int L, int NTOK>
-#ifdef VC
-using NarrowFor = Narrow<L, NTOK, VC, VD>;
-#else
-using NarrowFor = Narrow<L, NTOK, L == TERN_Q2_0_G128 ? (NTOK == 1 ? 4 : 2) : L == TERN_T3_5PB_G128 && NTOK == 1 ? 2 : 1,
-                         L == TERN_Q2_0_G128 ? (NTOK == 1 ? 2 : 3) : L == TERN_T3_5PB_G128 && NTOK == 1 ? 2 : 4>;
-#endif
 
 }  // namespace rows
 }  // namespace tern
