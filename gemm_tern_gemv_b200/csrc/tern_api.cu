@@ -390,7 +390,7 @@ static tern_status check_moe(const tern_moe_layer* L, int64_t tokens) {
 
 size_t tern_moe_workspace_bytes(const tern_moe_layer* layer, int64_t tokens) {
   if (check_moe(layer, tokens) != TERN_OK) return 0;
-  return moe_plan(tokens, layer->gate_up->k, layer->down->k, layer->top_k).bytes;
+  return moe_plan(layer->down->layout, tokens, layer->gate_up->k, layer->down->k, layer->experts, layer->top_k).bytes;
 }
 
 tern_status tern_moe(const tern_moe_layer* layer, const uint16_t* x, int64_t tokens, const uint16_t* residual, uint16_t* y,
@@ -402,7 +402,7 @@ tern_status tern_moe(const tern_moe_layer* layer, const uint16_t* x, int64_t tok
   if (!aligned2(y) || !aligned2(residual) || (reinterpret_cast<uintptr_t>(weights) & 3u) ||
       (reinterpret_cast<uintptr_t>(ids) & 3u))
     return TERN_ERR_ALIGNMENT;
-  const MoePlan plan = moe_plan(tokens, layer->gate_up->k, layer->down->k, layer->top_k);
+  const MoePlan plan = moe_plan(layer->down->layout, tokens, layer->gate_up->k, layer->down->k, layer->experts, layer->top_k);
   if (!workspace || workspace_bytes < plan.bytes) return TERN_ERR_WORKSPACE;
   if (!aligned16(workspace)) return TERN_ERR_ALIGNMENT;
   MoeParams p{};

@@ -140,13 +140,15 @@ struct MoeParams {
   float* weights;            // [tokens][top_k]
   int32_t* ids;              // [tokens][top_k]
   uint32_t* clear;           // largest |h| of each (token, expert) pair as bits, then a counter per 16 columns of y
-  float *h, *z;              // [tokens * top_k][f] expert activations, [tokens * top_k][d] their down products
+  float *h, *z;              // [tokens * top_k][f] expert activations, [slices][tokens * top_k][d] down products
+  int slices;                // of the down products' K
   int tokens, d, f, experts, top_k, act, renormalize;
 };
 struct MoePlan {  // workspace offsets
   size_t ids, weights, clear, h, z, bytes;
+  int slices;  // see MoeParams
 };
-MoePlan moe_plan(int64_t tokens, int64_t d, int64_t f, int top_k);
+MoePlan moe_plan(int32_t down_layout, int64_t tokens, int64_t d, int64_t f, int experts, int top_k);
 cudaError_t launch_moe(const tern_matrix& G, const tern_matrix& D, MoeParams p, const MoePlan& plan, void* workspace,
                        cudaStream_t st);
 

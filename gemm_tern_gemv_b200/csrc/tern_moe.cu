@@ -17,7 +17,7 @@
 namespace tern {
 namespace {
 
-constexpr int kRouteCtas = 8, kRouteThreads = 256;
+constexpr int kRouteCtas = 8, kRouteThreads = 256, kCombineThreads = 128;
 constexpr int kMaxPairs = TERN_MOE_MAX_TOKENS * TERN_MOE_MAX_TOP_K;
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -61,8 +61,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
   const int rank = (int)cluster_rank();
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
-  for (int i = (int)(blockIdx.x * kRouteThreads + threadIdx.x); i < p.tokens * p.top_k + p.d / 8; i += (int)gridDim.x * kRouteThreads)
-    p.clear[i] = 0;  // largest |h| of each pair, then the strips' counters
+  for (int i = (int)(blockIdx.x * kRouteThreads + threadIdx.x); i < p.tokens * p.top_k; i += (int)gridDim.x * kRouteThreads)
+    p.clear[i] = 0;  // largest |h| of each pair
   for (int i = rank + kRouteCtas * warp; i < p.experts * parts; i += kWarps) {
     const int e = i / parts, v0 = p.d / 8 * (i % parts) / parts, v1 = p.d / 8 * (i % parts + 1) / parts;
     double s[TOK][4] = {};  // four sums each: fp64 additions take long one after the other
@@ -103,51 +103,39 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
   }
   // One warp per token; lane l holds the logits of experts l, l + 32, ... as 64-bit keys whose unsigned order
   // is the logits' (NaN last). Each pick is three warp reductions: high word, low word, lowest index.
-  const int t = t0 + warp, per = (p.experts + 31) / 32;
-  double mx = -INFINITY;
-  for (int i = 0; i < per; i++)
-    if (lane + 32 * i < p.experts) mx = fmax(mx, logit[warp][lane + 32 * i]);
-  for (int o = 16; o; o >>= 1) mx = fmax(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float sum = 0.f;
-  for (int i = 0; i < per; i++)
-    if (lane + 32 * i < p.experts) sum += exp_exact(logit[warp][lane + 32 * i] - mx);
-  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  uint32_t used = 0;  // bit i: expert lane + 32 i is taken
-  float chosen = 0.f, mine = 0.f;
-  uint64_t best = 0;
-  int be = -1;
-  bool stale = true;  // the lane's best is to be looked for
+  const int t = t0 + warp;
+  uint64_t key[kMoeMaxExperts / 32];
+#pragma unroll
+  for (int i = 0; i < kMoeMaxExperts / 32; i++) key[i] = lane + 32 * i < p.experts ? order_key(logit[warp][lane + 32 * i]) : 0;
+  int mine = 0;  // lane j: pick j
   for (int j = 0; j < p.top_k; j++) {
-    if (stale) {
-      best = 0;
-      be = -1;
-      for (int i = 0; i < per; i++) {
-        const int e = lane + 32 * i;
-        if (e >= p.experts || (used >> i & 1)) continue;
-        const uint64_t k = order_key(logit[warp][e]);
-        if (be < 0 || k > best) {
-          best = k;
-          be = e;
-        }
+    uint64_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < kMoeMaxExperts / 32; i++)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
       }
-      stale = false;
-    }
-    const uint32_t hi = be >= 0 ? (uint32_t)(best >> 32) : 0u, top = __reduce_max_sync(0xffffffffu, hi);
-    const bool in = be >= 0 && hi == top;
-    const uint32_t low = __reduce_max_sync(0xffffffffu, in ? (uint32_t)best : 0u);
-    const uint32_t e = __reduce_min_sync(0xffffffffu, in && (uint32_t)best == low ? (uint32_t)be : 0xffffu);
-    if ((int)e == be) {
-      used |= 1u << (e >> 5);
-      stale = true;
-    }
-    const float w = exp_exact(logit[warp][e] - mx) / sum;
-    chosen += w;
-    if (lane == j) {
-      mine = w;
-      p.ids[t * p.top_k + j] = (int)e;
-    }
+    const uint32_t hi = (uint32_t)(best >> 32), top = __reduce_max_sync(0xffffffffu, hi);
+    const uint32_t low = __reduce_max_sync(0xffffffffu, hi == top ? (uint32_t)best : 0u);
+    const uint32_t e = __reduce_min_sync(0xffffffffu, hi == top && (uint32_t)best == low ? (uint32_t)(lane + 32 * at) : 0xffffu);
+    if ((e & 31) == lane)
+#pragma unroll
+      for (int i = 0; i < kMoeMaxExperts / 32; i++)
+        if (i == (int)(e >> 5)) key[i] = 0;
+    if (lane == j) mine = (int)e;
   }
-  if (lane < p.top_k) p.weights[t * p.top_k + lane] = p.renormalize ? mine / chosen : mine;
+  const double mx = logit[warp][__shfl_sync(0xffffffffu, mine, 0)];
+  float sum = 0.f;
+  for (int e = lane; e < p.experts; e += 32) sum += exp_exact(logit[warp][e] - mx);
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float w = lane < p.top_k ? exp_exact(logit[warp][mine] - mx) / sum : 0.f;
+  float chosen = w;
+  for (int o = 8; o; o >>= 1) chosen += __shfl_xor_sync(0xffffffffu, chosen, o);
+  if (lane >= p.top_k) return;
+  p.ids[t * p.top_k + lane] = mine;
+  p.weights[t * p.top_k + lane] = p.renormalize ? w / chosen : w;
 }
 
 // ---- the experts ------------------------------------------------------------------------------------------
@@ -157,8 +145,6 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
 // together.
 constexpr int kPlans = 8;  // cuts for up to 1, 2, 3, 4, 6, 8, 16 and any number of tiles
 __host__ __device__ constexpr int plan_tiles(int i) { return i < 4 ? i + 1 : i == 4 ? 6 : i == 5 ? 8 : i == 6 ? 16 : 32; }
-
-constexpr int kMaxStrips = 128;  // strips (row tiles of the down matrix) between two looks at their counters
 
 struct Lists {
   int segments, tiles;             // chunks of pairs; row tiles of all of them
@@ -171,7 +157,6 @@ struct Lists {
   int index[16];                   // rows of the activations of the current segment
   float mul[16];                   // and their powers of two
   uint32_t top[16];                // largest |h| of each in this CTA
-  int last[kMaxStrips];            // strips that this CTA finished
 };
 
 // Sorts the pairs by expert, in their own order within it (every CTA has to cut the same segments), and cuts
@@ -243,7 +228,21 @@ struct ExpertParams {
   MoeParams p;
   rows::Mat mat;
   rows::Split split[kPlans];
+  int slices, slice_blocks;  // down: K cut into this many runs of blocks
 };
+// Blocks [b0, b0 + n) of K as a matrix of its own.
+template <int L>
+__device__ __forceinline__ rows::Mat slice_of(const rows::Mat& m, int b0, int n) {
+  constexpr int kBlockK = rows::kBlk * rows::Lay<L>::kUnitK, kGroups = kBlockK / kGroup;
+  rows::Mat s = m;
+  s.codes += b0 * 128;
+  s.scales += b0 * kGroups;
+  s.K = min(m.K - b0 * kBlockK, n * kBlockK);
+  s.row_bytes = min(m.row_bytes - b0 * 128, n * 128);
+  s.groups = min(m.groups - b0 * kGroups, n * kGroups);
+  s.units = min(m.units - b0 * rows::kBlk, n * rows::kBlk);
+  return s;
+}
 __device__ __forceinline__ const rows::Split& split_for(const ExpertParams& q, int tiles) {
   int i = 0;
   while (i < kPlans - 1 && plan_tiles(i) < tiles) i++;
@@ -295,12 +294,12 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int per = p.d / kStep, tid = threadIdx.x;
-  build_lists(p, s, P::kRows, per);
-  uint32_t* counter = p.clear + p.tokens * p.top_k;
+  build_lists(p, s, P::kRows, per * q.slices);
   const int t1 = (int)((int64_t)(blockIdx.x + 1) * s.tiles / gridDim.x);
 #pragma unroll 1
   for (int t = (int)((int64_t)blockIdx.x * s.tiles / gridDim.x); t < t1;) {
-    const int g = t / per, a = t % per, b = min(min(per, a + t1 - t), a + kMaxStrips), n = s.seg_count[g];
+    const int g = t / per / q.slices, sl = t / per % q.slices;  // segment and slice of K
+    const int a = t % per, b = min(per, a + t1 - t), n = s.seg_count[g];
     const uint16_t* pair = s.pair + s.seg_first[g];
     if (tid < n) {
       const int pr = pair[tid];
@@ -314,32 +313,48 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
     __syncthreads();
     const int64_t first = (int64_t)s.seg_expert[g] * p.d;
     P prod;
-    prod.run(smem, split_for(q, b - a), q.mat, rows::Map{first, first, p.d, kStep, kStep / 2}, a, b,
-             rows::FloatRows{p.h, p.f, s.index, s.mul}, n, [] {}, [&](int tile, int r, int c, float z, float) {
-               p.z[(int64_t)pair[c] * p.d + tile * kStep + r] = P::kMode == rows::kFp16 ? z / s.mul[c] : z;
+    float* zs = p.z + (int64_t)sl * p.tokens * p.top_k * p.d;
+    prod.run(smem, split_for(q, b - a), slice_of<L>(q.mat, sl * q.slice_blocks, q.slice_blocks),
+             rows::Map{first, first, p.d, kStep, kStep / 2}, a, b,
+             rows::FloatRows{p.h + sl * q.slice_blocks * rows::kBlk * rows::Lay<L>::kUnitK, p.f, s.index, s.mul}, n, [] {},
+             [&](int tile, int r, int c, float z, float) {
+               zs[(int64_t)pair[c] * p.d + tile * kStep + r] = P::kMode == rows::kFp16 ? z / s.mul[c] : z;
              });
-    // strips that now have the sums of every segment
-    __syncthreads();
-    if (tid < b - a) {
-      __threadfence();
-      s.last[tid] = atomicAdd(counter + a + tid, 1u) == (uint32_t)s.segments - 1u;
-      __threadfence();
-    }
-    __syncthreads();
-    for (int i = tid; i < (b - a) * kStep * p.tokens; i += rows::kThreads) {
-      const int r = i % kStep, tl = i / kStep % (b - a), tok = i / (kStep * (b - a));
-      if (!s.last[tl]) continue;
-      const int o = (a + tl) * kStep + r;
-      const int64_t at = (int64_t)tok * p.d + o;
-      float y = 0.f;
-#pragma unroll 4
-      for (int j = 0; j < p.top_k; j++) y = fmaf(p.weights[tok * p.top_k + j], __ldcg(p.z + (int64_t)(tok * p.top_k + j) * p.d + o), y);
-      if (p.residual) y += h2f(p.residual[at]);
-      p.y[at] = f2h(y);
-    }
     __syncthreads();
     t += b - a;
   }
+}
+
+// y = sum_j p_j (sum over the slices of z_j) (+ residual), four outputs a thread. (The last CTA at a strip of
+// outputs adding them up inside the down kernel left that to the few CTAs that the last segment is dealt to:
+// at 64 tokens, 8 experts of 4096 x 12288 the down kernel took 430 us so, against 144 and 5 for this one.)
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ MoeParams p) {
+  const int per = p.d / 4, i = (int)(blockIdx.x * kCombineThreads + threadIdx.x);
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
+  if (i >= p.tokens * per) return;
+  const int tok = i / per, pairs = p.tokens * p.top_k;
+  const int64_t at = (int64_t)tok * p.d + (i - tok * per) * 4;
+  float y[4] = {};
+  const float4* z = reinterpret_cast<const float4*>(p.z + (int64_t)tok * p.top_k * p.d) + (i - tok * per);
+#pragma unroll 4
+  for (int j = 0; j < p.top_k; j++) {
+    const float w = __ldcg(p.weights + tok * p.top_k + j);
+    float4 v = __ldcg(z + (int64_t)j * per);
+    for (int s = 1; s < p.slices; s++) {
+      const float4 u = __ldcg(z + ((int64_t)s * pairs + j) * per);
+      v.x += u.x;
+      v.y += u.y;
+      v.z += u.z;
+      v.w += u.w;
+    }
+    y[0] = fmaf(w, v.x, y[0]);
+    y[1] = fmaf(w, v.y, y[1]);
+    y[2] = fmaf(w, v.z, y[2]);
+    y[3] = fmaf(w, v.w, y[3]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; k++) p.y[at + k] = f2h(p.residual ? y[k] + h2f(p.residual[at + k]) : y[k]);
 }
 
 constexpr size_t kRoom = 227 * 1024 - (sizeof(Lists) + 1023) / 1024 * 1024 - 1024;  // dynamic shared memory
@@ -359,6 +374,9 @@ cudaError_t launch(const void* kern, int grid, int threads, size_t smem, cudaStr
   return cudaLaunchKernelExC(&cfg, kern, args);
 }
 
+// Blocks of each of s slices: an even number, since a base-3 block's scales are 10 bytes and are copied by words.
+int slice_blocks(int blocks, int s) { return s == 1 ? blocks : ((blocks + s - 1) / s + 1) / 2 * 2; }
+
 template <int L, bool UP, class P>
 cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t st) {
   ExpertParams q;
@@ -366,8 +384,11 @@ cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t s
   q.mat = rows::Mat{static_cast<const uint8_t*>(W.codes), W.scales, W.code_row_stride, W.scale_row_stride, (int)W.k,
                     (int)row_bytes(W.layout, W.k), (int)(W.k / kGroup), (int)((row_bytes(W.layout, W.k) + 31) / 32)};
   size_t smem = 0;
+  const int blocks = (q.mat.units + rows::kBlk - 1) / rows::kBlk;
+  q.slices = UP ? 1 : p.slices;
+  q.slice_blocks = slice_blocks(blocks, q.slices);
   for (int i = 0; i < kPlans; i++) {
-    if (!P::plan(plan_tiles(i), q.mat.units, kRoom, q.split + i)) return cudaErrorInvalidValue;
+    if (!P::plan(plan_tiles(i), std::min(q.mat.units, q.slice_blocks * rows::kBlk), kRoom, q.split + i)) return cudaErrorInvalidValue;
     smem = std::max(smem, P::smem_bytes(q.split[i]));
   }
   const void* kern = UP ? reinterpret_cast<const void*>(&moe_up_kernel<L, P>) : reinterpret_cast<const void*>(&moe_down_kernel<L, P>);
@@ -376,12 +397,38 @@ cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t s
   return launch(kern, sm_count(), rows::kThreads, smem, st, &q);
 }
 
+// f(form) with the form of the product that a call takes.
+template <class P> struct Form { using type = P; };
+template <int L, class F>
+auto with_form(int tokens, int top_k, int experts, F f) {
+  if (tokens == 1) return f(Form<rows::Product<L, rows::kInt8, 1>>{});
+  if (tokens == 2) return f(Form<rows::Product<L, rows::kInt8, 2 / rows::Geo<L, rows::kInt8>::kTok>>{});
+  if (tokens * top_k < 6 * experts) return f(Form<rows::Product<L, rows::kFp16, 1>>{});
+  return f(Form<rows::Product<L, rows::kFp16, 2>>{});
+}
+
 template <int L, bool UP>
 cudaError_t launch_experts(const tern_matrix& W, const MoeParams& p, cudaStream_t st) {
-  if (p.tokens == 1) return launch_form<L, UP, rows::Product<L, rows::kInt8, 1>>(W, p, st);
-  if (p.tokens == 2) return launch_form<L, UP, rows::Product<L, rows::kInt8, 2 / rows::Geo<L, rows::kInt8>::kTok>>(W, p, st);
-  if (p.tokens * p.top_k < 6 * p.experts) return launch_form<L, UP, rows::Product<L, rows::kFp16, 1>>(W, p, st);
-  return launch_form<L, UP, rows::Product<L, rows::kFp16, 2>>(W, p, st);
+  return with_form<L>(p.tokens, p.top_k, p.experts, [&](auto form) { return launch_form<L, UP, typename decltype(form)::type>(W, p, st); });
+}
+
+// Slices of K for the down products: the fewest (up to eight) whose operands stay in shared memory while a CTA
+// goes down the rows. (Passes over K inside a CTA build them again for every few tiles: 8 experts of
+// 4096 x 12288 at 64 tokens took 333 us so, 144 with three slices.) A slice is not empty.
+template <int L>
+int down_slices(int64_t f, int tokens, int top_k, int experts) {
+  const int units = (int)((row_bytes(L, f) + 31) / 32), blocks = (units + rows::kBlk - 1) / rows::kBlk;
+  return with_form<L>(tokens, top_k, experts, [&](auto form) {
+    using P = typename decltype(form)::type;
+    int s = 1;
+    for (; s < 8; s++) {
+      const int n = slice_blocks(blocks, s);
+      rows::Split split;
+      if (P::plan(32, std::min(units, n * rows::kBlk), kRoom, &split) && split.pass >= n) break;
+    }
+    const int n = slice_blocks(blocks, s);
+    return (blocks + n - 1) / n;
+  });
 }
 
 template <bool UP>
@@ -395,16 +442,19 @@ cudaError_t dispatch(const tern_matrix& W, const MoeParams& p, cudaStream_t st) 
 
 }  // namespace
 
-MoePlan moe_plan(int64_t tokens, int64_t d, int64_t f, int top_k) {
+MoePlan moe_plan(int32_t down_layout, int64_t tokens, int64_t d, int64_t f, int experts, int top_k) {
   MoePlan w{};
+  w.slices = down_layout == TERN_Q2_0_G128     ? down_slices<TERN_Q2_0_G128>(f, (int)tokens, top_k, experts)
+             : down_layout == TERN_T3_5PB_G128 ? down_slices<TERN_T3_5PB_G128>(f, (int)tokens, top_k, experts)
+                                               : down_slices<TERN_Q1_0_G128>(f, (int)tokens, top_k, experts);
   const size_t pairs = (size_t)tokens * top_k;
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o += (bytes + 255) / 256 * 256; return at; };
   w.ids = take(pairs * 4);
   w.weights = take(pairs * 4);
-  w.clear = take((pairs + d / 8) * 4);
+  w.clear = take(pairs * 4);
   w.h = take(pairs * f * 4);
-  w.z = take(pairs * d * 4);
+  w.z = take(w.slices * pairs * d * 4);
   w.bytes = o;
   return w;
 }
@@ -417,6 +467,7 @@ cudaError_t launch_moe(const tern_matrix& G, const tern_matrix& D, MoeParams p, 
   p.clear = reinterpret_cast<uint32_t*>(ws + w.clear);
   p.h = reinterpret_cast<float*>(ws + w.h);
   p.z = reinterpret_cast<float*>(ws + w.z);
+  p.slices = w.slices;
   const int tok = p.tokens > 32 ? 4 : p.tokens > 16 ? 2 : 1;
   const void* route = tok == 4   ? reinterpret_cast<const void*>(&route_kernel<4>)
                       : tok == 2 ? reinterpret_cast<const void*>(&route_kernel<2>)
@@ -425,7 +476,9 @@ cudaError_t launch_moe(const tern_matrix& G, const tern_matrix& D, MoeParams p, 
   if (e != cudaSuccess) return e;
   e = dispatch<true>(G, p, st);
   if (e != cudaSuccess) return e;
-  return dispatch<false>(D, p, st);
+  e = dispatch<false>(D, p, st);
+  if (e != cudaSuccess) return e;
+  return launch(reinterpret_cast<const void*>(&combine_kernel), (p.tokens * (p.d / 4) + kCombineThreads - 1) / kCombineThreads, kCombineThreads, 0, st, &p);
 }
 
 }  // namespace tern

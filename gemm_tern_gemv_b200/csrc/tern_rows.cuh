@@ -70,6 +70,19 @@ __device__ __forceinline__ void mma_u8(int (&d)[4], uint32_t a0, uint32_t a1, ui
                : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
                : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The first of a chain, on accumulators that start at c0 and c1 in both rows.
+__device__ __forceinline__ void mma_u8_first(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                             uint32_t b1, int c0, int c1) {
+  asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
+               : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(c0), "r"(c1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                              uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+               : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+               : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -320,19 +333,20 @@ struct Split {
 // A block is four units, 128 bytes of a row: what a warp copies and works off at a time.
 constexpr int kBlk = 4;
 
-// Code operands a0 .. a3 of each int8 MMA from 8 bytes of rows g (a) and g + 8 (b). k85, kc80: 85 and 80 in
-// both halves, opaque to the compiler so that the base-3 steps stay multiplications.
+// Code operands a0 .. a3 of each int8 MMA from 8 bytes of rows g (a) and g + 8 (b). kx, ky are constants opaque
+// to the compiler: base-3's 85 and 80 in both halves, so that its steps stay multiplications; Q2's 0xAA..,
+// so that flipping and masking are one three-input operation.
 template <int L>
-__device__ __forceinline__ void operands8(uint2 a, uint2 b, uint32_t k85, uint32_t kc80, uint32_t (&F)[4][Geo<L, kInt8>::kPairs * 2]) {
+__device__ __forceinline__ void operands8(uint2 a, uint2 b, uint32_t kx, uint32_t ky, uint32_t (&F)[4][Geo<L, kInt8>::kPairs * 2]) {
   const uint32_t w[4] = {a.x, b.x, a.y, b.y};
 #pragma unroll
   for (int i = 0; i < 4; i++) {
     if constexpr (L == TERN_Q2_0_G128) {
       const uint32_t z = w[i] >> 4;
-      F[i][0] = (w[i] ^ 0xAAAAAAAAu) & 0x03030303u;
-      F[i][1] = (w[i] ^ 0xAAAAAAAAu) & 0x0C0C0C0Cu;
-      F[i][2] = (z ^ 0xAAAAAAAAu) & 0x03030303u;
-      F[i][3] = (z ^ 0xAAAAAAAAu) & 0x0C0C0C0Cu;
+      F[i][0] = (w[i] ^ kx) & 0x03030303u;
+      F[i][1] = (w[i] ^ kx) & 0x0C0C0C0Cu;
+      F[i][2] = (z ^ kx) & 0x03030303u;
+      F[i][3] = (z ^ kx) & 0x0C0C0C0Cu;
     } else if constexpr (L == TERN_Q1_0_G128) {
       const uint32_t z = w[i] >> 4;
 #pragma unroll
@@ -345,8 +359,8 @@ __device__ __forceinline__ void operands8(uint2 a, uint2 b, uint32_t k85, uint32
       F[i][0] = w[i];
 #pragma unroll
       for (int j = 1; j <= 4; j++) {
-        E = E * k85 + kc80;
-        O = O * k85 + kc80;
+        E = E * kx + ky;
+        O = O * kx + ky;
         F[i][j] = __byte_perm(E, O, 0x7351);
         if (j < 4) {
           E = __byte_perm(E, 0u, 0x4341);
@@ -385,7 +399,7 @@ struct Product {
   const uint8_t* pc[4];
   const uint16_t* ps;
   int lt, lb;
-  uint32_t k85, kc80;  // opaque to the compiler, so that the base-3 steps stay multiplications
+  uint32_t kx, ky;  // see operands8
 
   __device__ __forceinline__ void set_rows(const Mat& M, const Map& R) {
     const int lane = threadIdx.x & 31;
@@ -423,22 +437,11 @@ struct Product {
     const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
     if constexpr (MODE == kInt8) {
       int c[NT][4];
-      float sc[NT];
-      int add[NT];
+      uint4 st[NT];  // accumulator starts (binary: what twice the accumulators need added) and 2^-S
 #pragma unroll
-      for (int n = 0; n < NT; n++) {
-        const uint4 r = lds128(hd + (uint32_t)(n * G::kTileBytes));
-        if (L == TERN_Q1_0_G128) {
-          add[n] = (int)r.x;
-          c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0;
-        } else {
-          c[n][0] = c[n][2] = (int)r.x;
-          c[n][1] = c[n][3] = (int)r.y;
-        }
-        sc[n] = __uint_as_float(r.z);
-      }
+      for (int n = 0; n < NT; n++) st[n] = lds128(hd + (uint32_t)(n * G::kTileBytes));
       uint32_t F[4][G::kPairs * 2];
-      operands8<L>(a, b, k85, kc80, F);
+      operands8<L>(a, b, kx, ky, F);
 #pragma unroll
       for (int p = 0; p < G::kPairs; p++)
 #pragma unroll
@@ -446,24 +449,24 @@ struct Product {
           // binary: the columns of the other slot are zero
           const uint32_t at = base + ent[n] + (uint32_t)(n * G::kTileBytes + p * G::kEnt * 16);
           const uint4 f = L == TERN_Q1_0_G128 ? lds128_if(at, (g >> 2) == (q >> 1)) : lds128(at);
-          mma_u8(c[n], F[0][2 * p], F[1][2 * p], F[2][2 * p], F[3][2 * p], f.x, f.y);
+          if (p == 0) mma_u8_first(c[n], F[0][0], F[1][0], F[2][0], F[3][0], f.x, f.y, L == TERN_Q1_0_G128 ? 0 : (int)st[n].x, L == TERN_Q1_0_G128 ? 0 : (int)st[n].y);
+          else mma_u8(c[n], F[0][2 * p], F[1][2 * p], F[2][2 * p], F[3][2 * p], f.x, f.y);
           if (2 * p + 1 < G::kMma) mma_u8(c[n], F[0][2 * p + 1], F[1][2 * p + 1], F[2][2 * p + 1], F[3][2 * p + 1], f.z, f.w);
         }
 #pragma unroll
       for (int n = 0; n < NT; n++) {
         int v0 = c[n][0] + 256 * c[n][1], v1 = c[n][2] + 256 * c[n][3];
         if (L == TERN_Q1_0_G128) {  // t = 2 b - 1
-          v0 = 2 * v0 + add[n];
-          v1 = 2 * v1 + add[n];
+          v0 = 2 * v0 + (int)st[n].x;
+          v1 = 2 * v1 + (int)st[n].x;
         }
-        acc[n][0] = fmaf(s0 * sc[n], (float)v0, acc[n][0]);
-        acc[n][1] = fmaf(s1 * sc[n], (float)v1, acc[n][1]);
+        const float sc = __uint_as_float(st[n].z);
+        acc[n][0] = fmaf(s0 * sc, (float)v0, acc[n][0]);
+        acc[n][1] = fmaf(s1 * sc, (float)v1, acc[n][1]);
       }
     } else {
       const uint32_t w[4] = {a.x, b.x, a.y, b.y};
       float c[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; n++) c[n][0] = c[n][1] = c[n][2] = c[n][3] = 0.f;
       uint32_t O[4][L == TERN_T3_5PB_G128 ? 10 : 1];
       if constexpr (L == TERN_T3_5PB_G128) {
 #pragma unroll
@@ -482,7 +485,8 @@ struct Product {
         for (int n = 0; n < NT; n++) {
           const uint32_t at = base + ent[n] + (uint32_t)(n * G::kTileBytes + p * G::kEnt * 16);
           const uint4 f = L == TERN_Q1_0_G128 ? lds128_if(at, (g >> 2) == (q >> 1)) : lds128(at);
-          mma_f16(c[n], a00, a01, a02, a03, f.x, f.y);
+          if (p == 0) mma_f16_first(c[n], a00, a01, a02, a03, f.x, f.y);
+          else mma_f16(c[n], a00, a01, a02, a03, f.x, f.y);
           mma_f16(c[n], a10, a11, a12, a13, f.z, f.w);
         }
       }
@@ -547,11 +551,12 @@ struct Product {
     int* odd = reinterpret_cast<int*>(tail);  // rows of x with a non-finite activation
     uint32_t* scr = reinterpret_cast<uint32_t*>(tail + 64) + warp * 256;
     const uint32_t ring = ((sm100::smem_u32(tail) + 64 + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 127) & ~127u) + warp * (kDepth * kStage);
-    const int kg = warp % s.wk, tg = warp / s.wk;
     const int blocks = (M.units + kBlk - 1) / kBlk;
-    k85 = 85u;
-    kc80 = 0x00500050u;
-    asm volatile("" : "+r"(k85), "+r"(kc80));
+    const int wk = min(s.wk, blocks);  // (M may be shorter than what was planned for)
+    const int kg = warp % wk, tg = warp / wk;
+    kx = L == TERN_Q2_0_G128 ? 0xAAAAAAAAu : 85u;
+    ky = 0x00500050u;
+    asm volatile("" : "+r"(kx), "+r"(ky));
     // This lane's entry of a column tile's operands: column g, k by q. Columns of absent rows of x read
     // those of a present one (their sums are never looked at).
     uint32_t ent[NT];
@@ -585,7 +590,7 @@ struct Product {
       }
       for (int p0 = 0; p0 < blocks; p0 += s.pass) {
         const int p1 = min(blocks, p0 + s.pass);
-        const int lo = p0 + (p1 - p0) * kg / s.wk, hi = p0 + (p1 - p0) * (kg + 1) / s.wk;  // the warp's blocks
+        const int lo = p0 + (p1 - p0) * kg / wk, hi = p0 + (p1 - p0) * (kg + 1) / wk;  // the warp's blocks
         int left = (tb - ta) * (hi - lo);  // blocks still to be copied
         const int total = left;
         lt = ta;
@@ -638,7 +643,7 @@ struct Product {
         float acc[NT][kAcc] = {};
         int cb = lo;
         uint32_t stage = ring;
-        float* out = part + (size_t)((ta - b0) * s.wk + kg) * 16 * kRows;
+        float* out = part + (size_t)((ta - b0) * wk + kg) * 16 * kRows;
 #pragma unroll 1
         for (int i = 0; i < total; i++) {
           copy_wait<kDepth - 1>();
@@ -674,7 +679,7 @@ struct Product {
           if (++cb == hi) {
             store_part(out, p0 > 0, acc);
             cb = lo;
-            out += s.wk * 16 * kRows;
+            out += wk * 16 * kRows;
           }
         }
         copy_wait<0>();
@@ -687,10 +692,10 @@ struct Product {
         const int r = i & (rows - 1), tt = i >> shift, t = tokens == 1 ? 0 : tt % tokens, tl = tokens == 1 ? tt : tt / tokens;
         const int64_t o = (int64_t)(b0 + tl) * R.step + r;
         if (o >= R.limit) continue;
-        const float* x = part + (size_t)tl * s.wk * 16 * kRows + r * kRows + t;
+        const float* x = part + (size_t)tl * wk * 16 * kRows + r * kRows + t;
         float z0 = 0.f, z1 = 0.f;
 #pragma unroll 4
-        for (int w = 0; w < s.wk; w++) {
+        for (int w = 0; w < wk; w++) {
           z0 += x[w * 16 * kRows];
           if (pairs) z1 += x[(w * 16 + 8) * kRows];
         }
@@ -734,9 +739,9 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
     const double per_group = (double)((s.batch + s.tg - 1) / s.tg);  // tiles of a tile group in a batch
     const double work = per_group * ((s.pass + wk - 1) / wk + 0.5);
     double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * blocks : 0.0);
-    // warps side by side along K read a row's bytes together; far fewer than 1 KB of it at a time cost DRAM its
-    // open pages (16 warps on 16 tiles of their own: a third of the rate)
-    const int together = std::min(blocks, 8);
+    // warps side by side along K read a row's bytes together; much less than 512 of them at a time cost DRAM its
+    // open pages (24576 x 4096 Q2, one row: 13.6 us with 4, 8 or 16 warps along K, 14.2 with 2)
+    const int together = std::min(blocks, 4);
     if (wk < together) cost *= 0.5 + 0.5 * together / wk;
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;

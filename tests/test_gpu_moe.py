@@ -159,3 +159,10 @@ def test_refused_operands():
                dict(x=x[:0]), dict(down=lay.G), dict(workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(T.TernError):
             T.moe(**{"gate_up": lay.G, "down": lay.D, "router": r, "x": x, "top_k": 2, **kw})
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("tokens,f", [(2, 16384), (20, 6400), (40, 12416)])
+def test_long_down_rows(layout, tokens, f):
+    # down products whose K is cut into slices
+    Layer(layout, 128, f, 2, seed=15).check(half(11, tokens, 128), 1, residual=half(12, tokens, 128))
