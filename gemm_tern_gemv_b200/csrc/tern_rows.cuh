@@ -728,24 +728,25 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
     Split s{wk, std::max(1, std::min(kMaxWarps / wk, tiles)), 0, 0};
     const size_t tile_bytes = (size_t)wk * 16 * P::kRows * 4, fixed = P::smem_bytes(Split{wk, 1, 0, 0});
     const size_t block_bytes = (size_t)kBlk * P::kUnitBytes;
-    // up to a quarter of the room for partial sums, but one tile for each tile group at least
-    s.batch = std::min<int>(tiles, std::max<int>(s.tg, (int)std::min<size_t>(room / 4 / tile_bytes, 64)));
-    if (fixed + s.batch * tile_bytes + wk * block_bytes > room) continue;  // a block for each warp along K
-    s.pass = (int)std::min<size_t>(blocks, (room - fixed - s.batch * tile_bytes) / block_bytes);
-    // balanced passes; the first one gives every chunk a block, so every partial sum is written
-    const int passes = (blocks + s.pass - 1) / s.pass;
-    s.pass = std::max(wk, (blocks + passes - 1) / passes);
-    const int batches = (tiles + s.batch - 1) / s.batch;
-    const double per_group = (double)((s.batch + s.tg - 1) / s.tg);  // tiles of a tile group in a batch
-    const double work = per_group * ((s.pass + wk - 1) / wk + 0.5);
-    double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * blocks : 0.0);
-    // warps side by side along K read a row's bytes together; much less than 512 of them at a time cost DRAM its
-    // open pages (24576 x 4096 Q2, one row: 13.6 us with 4, 8 or 16 warps along K, 14.2 with 2)
-    const int together = std::min(blocks, 4);
-    if (wk < together) cost *= 0.5 + 0.5 * together / wk;
-    if (best_cost < 0 || cost < best_cost) {
-      best_cost = cost;
-      best = s;
+    // batches of one, two, ... tiles for each group, up to a quarter of the room for partial sums
+    for (int each = 1; each == 1 || (s.batch < tiles && s.batch < 64 && (size_t)s.batch * tile_bytes < room / 4); each++) {
+      s.batch = std::min(tiles, each * s.tg);
+      if (fixed + s.batch * tile_bytes + wk * block_bytes > room) break;  // a block for each warp along K
+      s.pass = (int)std::min<size_t>(blocks, (room - fixed - s.batch * tile_bytes) / block_bytes);
+      // balanced passes; the first one gives every chunk a block, so every partial sum is written
+      const int passes = (blocks + s.pass - 1) / s.pass;
+      s.pass = std::max(wk, (blocks + passes - 1) / passes);
+      const int batches = (tiles + s.batch - 1) / s.batch;
+      const double work = (double)((s.batch + s.tg - 1) / s.tg) * ((s.pass + wk - 1) / wk + 0.5);
+      double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * blocks : 0.0);
+      // warps side by side along K read a row's bytes together; much less than 512 of them at a time cost DRAM
+      // its open pages (24576 x 4096 Q2, one row: 13.6 us with 4, 8 or 16 warps along K, 14.2 with 2)
+      const int together = std::min(blocks, 4);
+      if (wk < together) cost *= 0.9 + 0.1 * together / wk;
+      if (best_cost < 0 || cost < best_cost) {
+        best_cost = cost;
+        best = s;
+      }
     }
   }
   *out = best;
