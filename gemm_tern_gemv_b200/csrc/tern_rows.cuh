@@ -620,8 +620,6 @@ struct Product {
         if (fresh || s.pass < blocks) {
           __syncthreads();  // the operands of the pass before are no longer read (and the flags are clear)
           const int u0 = p0 * kBlk, nu = min(M.units, p1 * kBlk) - u0;
-          for (uint32_t i = (uint32_t)nu * kUnitBytes + tid * 16; i < (uint32_t)(p1 * kBlk - u0) * kUnitBytes; i += kThreads * 16)
-            *reinterpret_cast<uint4*>(frag + i) = make_uint4(0, 0, 0, 0);  // units past the row's end
           if constexpr (MODE == kInt8) {
 #pragma unroll 1
             for (int t = 0; t < tokens; t++)
@@ -671,11 +669,14 @@ struct Product {
             b[j] = lds64(at + 8 * 128);
           }
           __syncwarp();  // every lane has read the stage
+          const int have = M.units - cb * kBlk;
           next(stage);
           stage = stage == ring + (kDepth - 1) * kStage ? ring : stage + kStage;
 #pragma unroll
-          for (int j = 0; j < kBlk; j++)
+          for (int j = 0; j < kBlk; j++) {
+            if (j >= have) break;  // the row ends inside the block
             unit(a[j], b[j], h2f((uint16_t)sa[j]), h2f((uint16_t)sb[j]), base0 + fo + j * kUnitBytes, hd0 + fo + j * kUnitBytes, ent, acc);
+          }
           if (++cb == hi) {
             store_part(out, p0 > 0, acc);
             cb = lo;
@@ -728,8 +729,8 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
     Split s{wk, std::max(1, std::min(kMaxWarps / wk, tiles)), 0, 0};
     const size_t tile_bytes = (size_t)wk * 16 * P::kRows * 4, fixed = P::smem_bytes(Split{wk, 1, 0, 0});
     const size_t block_bytes = (size_t)kBlk * P::kUnitBytes;
-    // batches of one, two, ... tiles for each group, up to a quarter of the room for partial sums
-    for (int each = 1; each == 1 || (s.batch < tiles && s.batch < 64 && (size_t)s.batch * tile_bytes < room / 4); each++) {
+    // batches of one, two, four, ... tiles for each group, up to a quarter of the room for partial sums
+    for (int each = 1; each == 1 || (s.batch < tiles && s.batch < 64 && (size_t)s.batch * tile_bytes < room / 4); each *= 2) {
       s.batch = std::min(tiles, each * s.tg);
       if (fixed + s.batch * tile_bytes + wk * block_bytes > room) break;  // a block for each warp along K
       s.pass = (int)std::min<size_t>(blocks, (room - fixed - s.batch * tile_bytes) / block_bytes);
