@@ -16,7 +16,9 @@
 //   * Warps: 0 and 2 TMA, 1 MMA, 4-11 epilogue (two for each 32 rows of A, every other 16 columns each), 12 on
 //     decode (three sets of four; a set takes every third stage, which hides the latencies between a stage's
 //     arrival and its decoded weights').
-//   * bn is chosen by the host so that the tiles fill whole waves of CTAs.
+//   * bn is chosen by the host so that the tiles fill whole waves of CTAs. Where there are few tiles, two to four
+//     pairs in a cluster take a part of a tile's sum each and exchange the accumulators through each other's
+//     shared memory, in a fixed order.
 //   * Transposed: A's rows are the columns of the packed rows, whose group is one scale per packed row.
 //     ldmatrix.trans hands a lane 16-bit pieces of two adjacent rows; each field of theirs is a finished
 //     pair of A, and the 16x128b store shape has rows by lane / 4 and columns by lane % 4 as ldmatrix has.
@@ -36,6 +38,7 @@ using namespace sm100;
 constexpr int BM = 128;      // rows of A per tile
 constexpr int BK = 64;       // terms per stage (one 128-byte swizzle row of fp16)
 constexpr int kMaxBN = 192;  // rows of x per tile (of a pair of CTAs)
+constexpr int kMaxSplits = 4;  // pairs that may share a tile's sum (a cluster of 8 CTAs)
 constexpr int STAGES = 8;    // TMA ring
 constexpr int ASTAGES = 8;   // A ring in tensor memory, at most: what the accumulators leave of it
 // 24 warps: the forward epilogue has more to do, the transposed decoding
@@ -65,6 +68,7 @@ struct Params {
   int64_t nout;          // outputs of a row: n, n / 2 (gated) or k (transposed)
   int terms;             // length of the sum: k or n
   int bn, rtiles, mtiles;
+  int splits;            // pairs of CTAs that share a tile's sum, up to kMaxSplits; if more than one, a pair has one tile
   const uint16_t* x;
   int64_t xstride;
   const uint8_t* codes;
@@ -124,18 +128,23 @@ __device__ __forceinline__ void tmem_relinquish_pair() {
 __device__ __forceinline__ void tmem_dealloc_pair(uint32_t taddr, uint32_t ncols) {
   asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
 }
-// Arrives on `bar` of both CTAs once every MMA issued before has completed.
-__device__ __forceinline__ void commit_both(uint64_t* bar) {
+// Arrives on `bar` of both CTAs (of cluster ranks first and first + 1) once every MMA issued before has completed.
+__device__ __forceinline__ void commit_both(uint64_t* bar, int first) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-               ::"r"(smem_u32(bar)), "h"((uint16_t)3) : "memory");
+               ::"r"(smem_u32(bar)), "h"((uint16_t)(3 << first)) : "memory");
 }
 __device__ __forceinline__ void commit_own(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-// Arrives on the first CTA's copy of `bar`.
-__device__ __forceinline__ void arrive_first(uint64_t* bar) {
+// Address of `local` in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(const void* local, int rank) {
   uint32_t remote;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(smem_u32(bar)));
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_u32(local)), "r"(rank));
+  return remote;
+}
+// Arrives on the copy of `bar` of the pair's first CTA.
+__device__ __forceinline__ void arrive_first(uint64_t* bar, int first) {
+  const uint32_t remote = in_cta(bar, first);
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 // Waits on a barrier that both CTAs arrive on.
@@ -315,7 +324,7 @@ __device__ __forceinline__ void finish_gated(const Params& p, uint32_t (&r)[16],
 
 // ---- the kernel ------------------------------------------------------------------------------------------
 template <int LAYOUT, bool TRANS>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -334,9 +343,13 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   volatile uint8_t* big = smem + OFF_BIG;
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int rank = (int)cluster_rank(), pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+  // the CTA's place in its pair, the pair's first CTA in the cluster, and the pair's slice of the sum; a cluster is
+  // `splits` pairs, `pair` and `pairs` count clusters
+  const int rank = (int)cluster_rank() & 1, first = (int)cluster_rank() - rank, slice = first / 2;
+  const int pair = (int)blockIdx.x / (2 * p.splits), pairs = (int)gridDim.x / (2 * p.splits);
   const int tiles = (p.rtiles + 1) / 2 * p.mtiles;  // of pairs
-  const int kblocks = (p.terms + BK - 1) / BK;
+  const int all_blocks = (p.terms + BK - 1) / BK;
+  const int first_kb = all_blocks * slice / p.splits, kblocks = all_blocks * (slice + 1) / p.splits - first_kb;
   const uint32_t a_col = 2 * p.bn, a_stages = min((kTmemCols - a_col) / 32, (uint32_t)ASTAGES);
   const bool gated = !TRANS && p.e.gated;
   const int step = gated ? 64 : BM;  // outputs of a tile
@@ -384,7 +397,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     bool dead = false;
     for (int tile = pair; tile < tiles; tile += pairs) {
       const int r0 = (tile / p.mtiles * 2 + rank) * step, m0 = (tile % p.mtiles) * p.bn + rank * (p.bn / 2);
-      for (int kb = 0; kb < kblocks; kb++) {
+      for (int kb = first_kb; kb < first_kb + kblocks; kb++) {
         if (!dead) dead = !mbar_wait_bounded(empty + s, ph, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
         dead = __any_sync(0xffffffffu, dead);
         if (elect_one() && !dead) {
@@ -442,9 +455,9 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         if (elect_one() && !dead) {
 #pragma unroll
           for (int kk = 0; kk < BK / 16; kk++) mma_f16_ts(tmem_d, a + 8 * kk, bdesc + 2 * kk, idesc, (kb | kk) != 0);
-          commit_both(empty + s);
-          commit_both(dempty + d);
-          if (kb == kblocks - 1) commit_both(tfull + acc);
+          commit_both(empty + s, first);
+          commit_both(dempty + d, first);
+          if (kb == kblocks - 1) commit_both(tfull + acc, first);
           issued = true;
         }
         __syncwarp();
@@ -483,19 +496,51 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       // the warps leave together, and have all read the tile's flags before any of them is cleared
       const bool fine = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
       volatile uint8_t* flag = big + (lt % kBigTiles) * BM + (TRANS ? 0 : quad * 32 + lane);
-      const bool again = LAYOUT != TERN_Q1_0_G128 && fine && *flag;
-      if (!bar_all(kEpiBarrier, kEpi * 32, fine)) break;
-      if (again) *flag = 0;
-      tc_fence_after();
       const uint32_t taddr = tmem + acc * p.bn + ((uint32_t)(quad * 32) << 16);
       const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);  // rows of x in this tile
+      bool again = LAYOUT != TERN_Q1_0_G128 && fine && *flag;
+      const bool go = bar_all(kEpiBarrier, kEpi * 32, fine);
+      if (p.splits > 1) {
+        // 16 columns at a time belong to the pairs in turn: what the others have of them comes to their owner
+        __syncwarp();
+        cluster_sync();  // the stages' memory is no longer in use anywhere in the cluster
+        if (go) {
+          tc_fence_after();
+          float* in = reinterpret_cast<float*>(smem) + quad * 32 + lane;
 #pragma unroll 1
-      for (int c0 = 4 * (warp & ~3) - 16; c0 < cols; c0 += 4 * kEpi) {
+          for (int c = (warp >> 2) - 1; 16 * c < cols; c += kEpi / 4) {
+            const int owner = c % p.splits;
+            if (owner == slice) continue;
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(taddr + 16 * c, r);
+            const uint32_t to = in_cta(in + ((c / p.splits) * (p.splits - 1) + slice - (slice > owner)) * 16 * BM, 2 * owner + rank);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; i++) asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(to + i * BM * 4), "r"(r[i]) : "memory");
+          }
+          if (again)
+            for (int i = 0; i < p.splits; i++)
+              asm volatile("st.shared::cluster.u8 [%0], %1;" ::"r"(in_cta(const_cast<uint8_t*>(flag), 2 * i + rank)), "r"(1) : "memory");
+        }
+        __syncwarp();
+        cluster_sync();
+        again = LAYOUT != TERN_Q1_0_G128 && *flag;
+      }
+      if (!go) break;
+      if (again && p.splits == 1) *flag = 0;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 16 * (slice + p.splits * ((warp >> 2) - 1)); c0 < cols; c0 += 4 * kEpi * p.splits) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(taddr + c0, r);
         const int lim = in ? cols - c0 : 0;  // rows of x that this lane writes
         const int64_t t0 = m0 + c0;
         tmem_ld_wait();
+        for (int i = 1; i < p.splits; i++) {
+          const float* in = reinterpret_cast<const float*>(smem) + ((c0 / 16 / p.splits) * (p.splits - 1) + i - 1) * 16 * BM + quad * 32 + lane;
+#pragma unroll
+          for (int q = 0; q < 16; q++) r[q] = __float_as_uint(__uint_as_float(r[q]) + in[q * BM]);
+        }
         if (again) {
 #pragma unroll
           for (int i = 0; i < 16; i++)
@@ -517,7 +562,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) arrive_first(tempty + acc);
+      if (lane == 0) arrive_first(tempty + acc, first);
     }
   } else if (warp >= kFirstDecoder) {
     // ------------------------------------------------------------------ decoders
@@ -538,6 +583,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       // block as a pair
       auto fetch = [&](int kb) -> uint32_t {
         if (kb >= kblocks || (TRANS && r0 >= p.k)) return 0;  // (the second CTA's columns may lie past the matrix)
+        kb += first_kb;
         if (!TRANS) return __ldg(srow + (kb * BK) / kGroup);
         const int64_t n = (int64_t)kb * BK + 2 * lane;
         const uint16_t* q = p.scales + n * p.sstride + r0 / kGroup;
@@ -561,7 +607,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
           const uint32_t s2 = cur | cur << 16;
           uint32_t o[32];
           if constexpr (LAYOUT == TERN_Q1_0_G128) {
-            const uint2 w = *reinterpret_cast<const uint2*>(P + src * 16 + 8 * (kb & 1));
+            const uint2 w = *reinterpret_cast<const uint2*>(P + src * 16 + 8 * ((first_kb + kb) & 1));
             pairs_q1(w.x, s2, o);
             pairs_q1(w.y, s2, o + 16);
           } else {
@@ -570,7 +616,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
               const uint4 u = *reinterpret_cast<const uint4*>(P + src * 16);
               w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
             } else {
-              t3_words(kb % 5, P + src * 32, lut + lane, w);
+              t3_words((first_kb + kb) % 5, P + src * 32, lut + lane, w);
             }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
@@ -638,7 +684,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) arrive_first(dfull + d);
+        if (lane == 0) arrive_first(dfull + d, first);
         flip ^= 1;
         s += SETS;
         if (s >= STAGES) {
@@ -651,12 +697,80 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     }
   }
 
+  if (p.splits > 1 && !(warp >= 4 && warp < kFirstDecoder)) {  // with the epilogue's warps: see there
+    __syncwarp();
+    cluster_sync();
+    cluster_sync();
+  }
   tc_fence_before();
   __syncthreads();
-  cluster_sync();  // neither CTA leaves while the other may still arrive on its barriers or read its operands
+  cluster_sync();  // no CTA leaves while another may still arrive on its barriers or read its operands
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
+  }
+}
+
+cudaLaunchConfig_t config(int clusters, int splits, cudaStream_t st, cudaLaunchAttribute* attr) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(clusters * 2 * splits));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = st;
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)(2 * splits);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cfg;
+}
+
+// Clusters of 2 x `splits` CTAs that run at the same time. The GPCs have different numbers of SMs, so this is less
+// than SMs / CTAs (74, 33, 22 and 15 for 1 to 4). Asked for once: other devices of a machine may differ a little,
+// which costs them time only.
+template <int LAYOUT, bool TRANS>
+int clusters_at_once(int splits) {
+  struct Counts {
+    int of[kMaxSplits + 1] = {};
+    Counts() {
+      const void* kern = reinterpret_cast<const void*>(&layer_gemm_kernel<LAYOUT, TRANS>);
+      if (allow_smem(kern, SMEM_BYTES) != cudaSuccess) return;
+      for (int i = 1; i <= kMaxSplits; i++) {
+        cudaLaunchAttribute attr[1];
+        cudaLaunchConfig_t cfg = config(1, i, nullptr, attr);
+        if (cudaOccupancyMaxActiveClusters(&of[i], kern, &cfg) != cudaSuccess) {
+          of[i] = 0;
+          (void)cudaGetLastError();
+        }
+      }
+    }
+  };
+  static const Counts counts;
+  return counts.of[splits];
+}
+
+// Rows of x per tile, the multiple of 32 up to kMaxBN, and pairs to a tile that make the waves of tiles cheapest.
+// 64 terms of a tile cost four MMAs of bn / 2 + 11 cycles, and no less than what the warps of an SM need to decode
+// them and to finish the tile before (about 480 cycles, measured at bn = 128 and 160). Two to four pairs share a
+// tile's sum where all tiles run at once then; bringing the sums together costs about kJoin cycles. (4096 x 12288
+// Q2 with 64 rows, 16 tiles: 58 us with one pair each, 30 with three.)
+template <int LAYOUT, bool TRANS>
+void pick_tiles(Params& p) {
+  constexpr int kJoin = 2500;
+  const int64_t blocks = (p.terms + BK - 1) / BK;
+  double cost = -1;
+  for (int bn = 32; bn <= kMaxBN; bn += 32) {
+    if (bn > 32 && bn - 32 >= p.m) break;
+    const int64_t tiles = ((int64_t)p.rtiles + 1) / 2 * ((p.m + bn - 1) / bn), waves = (tiles + sm_count() / 2 - 1) / (sm_count() / 2);
+    for (int splits = 1; splits <= kMaxSplits; splits++) {
+      if (splits > 1 && (tiles > (int64_t)clusters_at_once<LAYOUT, TRANS>(splits) || splits > blocks)) break;
+      const double c = (double)waves * ((blocks + splits - 1) / splits) * std::max(2 * bn + 44, 480) + (splits > 1 ? kJoin : 0);
+      if (cost < 0 || c < cost) {
+        cost = c;
+        p.bn = bn;
+        p.splits = splits;
+      }
+    }
   }
 }
 
@@ -665,6 +779,10 @@ cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, P
   CUtensorMap mx, mw;
   p.x = x;
   p.xstride = xstride;
+  pick_tiles<LAYOUT, TRANS>(p);
+  const int64_t mt = (p.m + p.bn - 1) / p.bn;
+  if (mt * p.rtiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
+  p.mtiles = (int)mt;
   if (!tmap_2d_new(&mx, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, x, (uint64_t)p.terms, (uint64_t)p.m, (uint64_t)xstride * 2, BK,
                    (uint32_t)p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
@@ -679,26 +797,10 @@ cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, P
   const cudaError_t e = allow_smem(kern, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)p.rtiles + 1) / 2 * p.mtiles;
-  layer_gemm_kernel<LAYOUT, TRANS><<<(unsigned)std::min<int64_t>(tiles, sm_count() / 2) * 2, kThreads, SMEM_BYTES, st>>>(mx, mw, p);
-  return cudaGetLastError();
-}
-
-// Rows of x per tile: the multiple of 32 up to kMaxBN that makes the waves of tiles cheapest. 64 terms of a
-// tile cost four MMAs of bn / 2 + 11 cycles, and no less than what the warps of an SM need to decode them and
-// to finish the tile before (about 480 cycles, measured at bn = 128 and 160).
-int pick_bn(int64_t m, int64_t rtiles, int sms) {
-  int best = kMaxBN;
-  double cost = -1;
-  for (int bn = 32; bn <= kMaxBN; bn += 32) {
-    if (bn > 32 && bn - 32 >= m) break;
-    const int64_t tiles = (rtiles + 1) / 2 * ((m + bn - 1) / bn), waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const double c = (double)waves * std::max(2 * bn + 44, 480);
-    if (cost < 0 || c < cost) {
-      cost = c;
-      best = bn;
-    }
-  }
-  return best;
+  const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, sm_count() / 2);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = config((int)clusters, p.splits, st, attr);
+  return cudaLaunchKernelEx(&cfg, &layer_gemm_kernel<LAYOUT, TRANS>, mx, mw, (const Params)p);
 }
 
 template <bool TRANS>
@@ -734,10 +836,6 @@ cudaError_t launch_layer_gemm(const tern_matrix& W, const uint16_t* x, int64_t m
   p.e = e;
   const int step = e.gated ? 64 : BM;
   p.rtiles = (int)((p.nout + step - 1) / step);
-  p.bn = pick_bn(m, p.rtiles, sm_count());
-  const int64_t mt = (m + p.bn - 1) / p.bn;
-  if (mt * p.rtiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-  p.mtiles = (int)mt;
   return dispatch<false>(W, x, W.k, p, st);
 }
 
@@ -748,10 +846,6 @@ cudaError_t launch_layer_gemm_t(const tern_matrix& W, const uint16_t* dz, int64_
   p.terms = (int)W.n;
   p.y = dx;
   p.rtiles = (int)(W.k / BM);
-  p.bn = pick_bn(m, p.rtiles, sm_count());
-  const int64_t mt = (m + p.bn - 1) / p.bn;
-  if (mt * p.rtiles > (int64_t)INT32_MAX) return cudaErrorInvalidValue;
-  p.mtiles = (int)mt;
   return dispatch<true>(W, dz, dz_stride, p, st);
 }
 

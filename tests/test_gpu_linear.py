@@ -286,3 +286,45 @@ def test_extreme_scales(layout, m, gated):
         fits = np.abs(want) < 65000
         check(np.where(fits, y, 0), np.where(fits, want, 0), bound, "extreme scales")
         assert np.isinf(y[~fits]).all() or fits.all()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n,k", [(1000, 2176), (2500, 1664), (8100, 1152), (72, 17408)])
+@pytest.mark.parametrize("m", [17, 48, 100, 191])
+def test_sums_shared_by_several_pairs(layout, n, k, m):
+    # few tiles with long rows: two or four pairs of blocks take a part of the sum each
+    _check(layout, m, n, k, act="gelu", bias=True, residual=True)
+    _check(layout, m, n, k, act="silu", gated=True, preact=True)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("m", [20, 90])
+def test_extreme_scale_in_one_part_of_the_sum(layout, m):
+    # only the blocks that meet the scale know of it; whoever finishes the output has to learn it
+    n, k = 300, 2304
+    codes, s, w = weights(layout, n, k, 74)
+    s[:] = np.float16(2.0 ** -16)
+    s[3, 0], s[140, 9], s[n - 1, 17] = 65504.0, -40000.0, 32768.0
+    w = np.sign(w) * np.repeat(s.astype(np.float64), 128, axis=1)
+    x = half(75, m, k, scale=2.0 ** -10)
+    y = T.linear(_matrix(codes, s, layout, k), _dev(x)).cpu().numpy()
+    want, bound = L.linear(w, f64(x), None, "none", False), L.linear_bound(w, f64(x), None, "none", False)
+    fits = np.abs(want) < 65000
+    check(np.where(fits, y, 0), np.where(fits, want, 0), bound, "one extreme scale")
+    assert np.isinf(y[~fits]).all() or fits.all()
+
+
+@pytest.mark.parametrize("m", [30, 150])
+def test_shared_sums_repeat_in_graphs(m):
+    W, _, x, _, r = _case(T.T3_5PB_G128, m, 1500, 2560, "none", False, False, True)
+    x, r = _dev(x), _dev(r)
+    want = T.linear(W, x, residual=r)
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=other):
+        ys = [T.linear(W, x, residual=r) for _ in range(3)]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want) for y in ys)

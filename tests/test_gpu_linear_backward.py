@@ -189,3 +189,24 @@ def test_extreme_scales(layout, m):
     dy = half(71, m, n, scale=2.0 ** -10)
     dx, _, _ = T.linear_backward(_matrix(codes, s, layout, k), _dev(dy))
     check(dx.cpu().numpy(), f64(dy) @ w, L.backward_bounds(w, f64(dy), None)[0], "extreme scales")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n,k", [(2600, 1024), (1500, 4096), (700, 7680), (9001, 128)])
+@pytest.mark.parametrize("m", [1, 33, 77, 190])
+def test_sums_shared_by_several_pairs(layout, n, k, m):
+    # few tiles of dx with many weight rows: two or four pairs of blocks take a part of the sum each
+    _check(layout, m, n, k, act="gelu_tanh")
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("m", [3, 100])
+def test_extreme_scale_in_one_part_of_the_sum(layout, m):
+    n, k = 2000, 384
+    codes, s, w = weights(layout, n, k, 74)
+    s[:] = np.float16(2.0 ** -16)
+    s[1999, 1] = -40000.0
+    w = np.sign(w) * np.repeat(s.astype(np.float64), 128, axis=1)
+    dy = half(75, m, n, scale=2.0 ** -10)
+    dx, _, _ = T.linear_backward(_matrix(codes, s, layout, k), _dev(dy))
+    check(dx.cpu().numpy(), f64(dy) @ w, L.backward_bounds(w, f64(dy), None)[0], "one extreme scale")
