@@ -35,6 +35,7 @@ struct RowsParams {
   Epilogue e;
   int64_t n, nout;
   int tiles, tokens, early;
+  int each, extra;  // tiles of a CTA; `extra` of the CTAs have one more
 };
 
 template <int L, class P>
@@ -42,7 +43,8 @@ __global__ void __launch_bounds__(rows::kThreads, 1) linear_rows_kernel(const __
   extern __shared__ __align__(16) uint8_t smem[];
   sm100::griddep_launch_dependents();
   if (!p.early) sm100::griddep_wait();
-  const int t0 = (int)((int64_t)blockIdx.x * p.tiles / gridDim.x), t1 = (int)((int64_t)(blockIdx.x + 1) * p.tiles / gridDim.x);
+  const int b = (int)blockIdx.x, ctas = (int)gridDim.x;
+  const int t0 = rows::first_tile(b, ctas, p.each, p.extra), t1 = rows::first_tile(b + 1, ctas, p.each, p.extra);
   const rows::HalfRows xs{p.x, p.mat.K, nullptr};
   P prod;
   prod.run(smem, p.split, p.mat, p.map, t0, t1, xs, p.tokens, [&] { if (p.early) sm100::griddep_wait(); },
@@ -60,6 +62,8 @@ cudaError_t launch_rows(RowsParams& p, cudaStream_t st) {
   p.map.ahead = p.e.gated ? 0 : step / 2;
   p.tiles = (int)((p.nout + step - 1) / step);
   const int grid = std::min(p.tiles, sm_count());
+  p.each = p.tiles / grid;
+  p.extra = p.tiles % grid;
   if (!P::plan((p.tiles + grid - 1) / grid, p.mat.units, kRoom, &p.split)) return cudaErrorInvalidValue;
   const size_t smem = P::smem_bytes(p.split);
   const cudaError_t err = allow_smem(reinterpret_cast<const void*>(&linear_rows_kernel<L, P>), kRoom);

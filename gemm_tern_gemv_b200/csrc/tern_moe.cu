@@ -243,6 +243,10 @@ __device__ __forceinline__ rows::Mat slice_of(const rows::Mat& m, int b0, int n)
   s.units = min(m.units - b0 * rows::kBlk, n * rows::kBlk);
   return s;
 }
+__device__ __forceinline__ int first_tile(int tiles, int b) {
+  const int ctas = (int)gridDim.x, each = tiles / ctas;
+  return rows::first_tile(b, ctas, each, tiles - each * ctas);
+}
 __device__ __forceinline__ const rows::Split& split_for(const ExpertParams& q, int tiles) {
   int i = 0;
   while (i < kPlans - 1 && plan_tiles(i) < tiles) i++;
@@ -259,9 +263,9 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_up_kernel(const __grid_
   sm100::griddep_wait();
   const int per = p.f / kStep;  // tiles of a segment
   build_lists(p, s, P::kRows, per);
-  const int t1 = (int)((int64_t)(blockIdx.x + 1) * s.tiles / gridDim.x);
+  const int t1 = first_tile(s.tiles, (int)blockIdx.x + 1);
 #pragma unroll 1
-  for (int t = (int)((int64_t)blockIdx.x * s.tiles / gridDim.x); t < t1;) {
+  for (int t = first_tile(s.tiles, (int)blockIdx.x); t < t1;) {
     const int g = t / per, a = t % per, b = min(per, a + t1 - t), n = s.seg_count[g];
     const uint16_t* pair = s.pair + s.seg_first[g];
     if ((int)threadIdx.x < n) {
@@ -295,9 +299,9 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
   sm100::griddep_wait();
   const int per = p.d / kStep, tid = threadIdx.x;
   build_lists(p, s, P::kRows, per * q.slices);
-  const int t1 = (int)((int64_t)(blockIdx.x + 1) * s.tiles / gridDim.x);
+  const int t1 = first_tile(s.tiles, (int)blockIdx.x + 1);
 #pragma unroll 1
-  for (int t = (int)((int64_t)blockIdx.x * s.tiles / gridDim.x); t < t1;) {
+  for (int t = first_tile(s.tiles, (int)blockIdx.x); t < t1;) {
     const int g = t / per / q.slices, sl = t / per % q.slices;  // segment and slice of K
     const int a = t % per, b = min(per, a + t1 - t), n = s.seg_count[g];
     const uint16_t* pair = s.pair + s.seg_first[g];

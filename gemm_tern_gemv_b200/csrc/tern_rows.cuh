@@ -182,21 +182,17 @@ struct FloatRows {
 };
 
 // ---- building the activation operands -----------------------------------------------------------------
-// int8 form of one (unit u, row t of x), the tok-th of its column tile. scr: 32 x 8 words of this warp;
+// int8 form of one unit u of one row of x, the tok-th of its column tile. xv: this lane's activations. scr: 32 x 8 words of this warp;
 // frag: the column tile's entries, then one 16-byte record for each q: accumulator starts of columns 2 q
 // and 2 q + 1 (binary: their sum to be added to twice the accumulators) and the scale 2^-S (x 2^16 for
 // digits 2 and 3). Non-finite activations count as zero here (the caller adds them apart) and set *odd.
-template <int L, class X>
-__device__ __forceinline__ void build_int8(const X& xs, int t, int tok, int u, int K, uint32_t* scr, uint4* frag, int* odd) {
+template <int L>
+__device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int tok, int u, uint32_t* scr, uint4* frag, int* odd) {
   using T = Lay<L>;
   using G = Geo<L, kInt8>;
   const int lane = threadIdx.x & 31;
   constexpr int NE = T::kUnitK / 32;  // activations of this lane: the weights of byte `lane` of the unit
   constexpr bool two_in_a_byte = L == TERN_T3_5PB_G128;  // a byte may hold weights of both slots
-  float xv[NE];
-#pragma unroll
-  for (int e = 0; e < NE; e++) xv[e] = 0.f;
-  xs.template load<NE>(t, u * T::kUnitK + lane * NE, K, xv);
   // first weight of the unit that belongs to slot 1
   const int edge = T::kSlots == 1 ? T::kUnitK : (L == TERN_Q1_0_G128 ? 128 : 128 - (u * 160) % 128);
   uint32_t mx[2] = {0, 0};
@@ -274,17 +270,23 @@ __device__ __forceinline__ void build_int8(const X& xs, int t, int tok, int u, i
   }
 }
 
-// fp16 form of one (unit, column tile): lane (g, q) writes the operand words of column g.
+// fp16 form of one (unit, column tile from row t0 of x on): lane (g, q) loads and writes the operand words of
+// column g.
+template <int L> constexpr int kLaneWords = Lay<L>::kUnitK / 8;  // pairs of activations a lane takes
 template <int L, class X>
-__device__ __forceinline__ void build_fp16(const X& xs, int t0, int tokens, int u, int K, uint4* frag) {
+__device__ __forceinline__ void load_fp16(const X& xs, int t0, int tokens, int u, int K, uint32_t (&v)[kLaneWords<L>]) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int tok = t0 + (L == TERN_Q2_0_G128 ? g : (g & 3));
+  if (tok < tokens && (L != TERN_Q1_0_G128 || (g >> 2) == (q >> 1))) xs.template load16<2 * kLaneWords<L>>(tok, Lay<L>::kUnitK * u + 2 * kLaneWords<L> * q, K, v);
+}
+template <int L>
+__device__ __forceinline__ void store_fp16(const uint32_t (&v)[kLaneWords<L>], int t0, int tokens, int u, uint4* frag) {
   using G = Geo<L, kFp16>;
   const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int tok = L == TERN_Q2_0_G128 ? g : (g & 3);
   if (t0 + tok >= tokens) return;
   if constexpr (L == TERN_T3_5PB_G128) {
-    uint32_t v[20];
     const int k0 = 160 * u + 40 * q;
-    xs.template load16<40>(t0 + tok, k0, K, v);
     const int edge = ((160 * u) / kGroup + 1) * kGroup - k0;  // first of the lane's weights in slot 1
     auto h = [&](int e) -> uint32_t {
       return ((e < edge) == (g < 4)) ? ((e & 1) ? v[e >> 1] >> 16 : v[e >> 1] & 0xffffu) : 0u;
@@ -294,22 +296,26 @@ __device__ __forceinline__ void build_fp16(const X& xs, int t0, int tokens, int 
 #pragma unroll
     for (int p = 0; p < 5; p++) frag[p * 32 + lane] = make_uint4(reg(0, 2 * p), reg(1, 2 * p), reg(0, 2 * p + 1), reg(1, 2 * p + 1));
   } else if constexpr (L == TERN_Q2_0_G128) {
-    uint32_t v[16];
-    xs.template load16<32>(t0 + tok, 128 * u + 32 * q, K, v);
 #pragma unroll
     for (int p = 0; p < 4; p++)  // register i: fields i and i + 8 of a word
       frag[p * 32 + lane] = make_uint4(__byte_perm(v[p], v[p + 4], 0x5410), __byte_perm(v[8 + p], v[12 + p], 0x5410),
                                        __byte_perm(v[p], v[p + 4], 0x7632), __byte_perm(v[8 + p], v[12 + p], 0x7632));
   } else {
     if ((g >> 2) != (q >> 1)) return;
-    uint32_t v[32];
-    xs.template load16<64>(t0 + tok, 256 * u + 64 * q, K, v);
 #pragma unroll
     for (int p = 0; p < 8; p++)  // register i: bits i and i + 16 of a word
       frag[p * G::kEnt + q * 4 + tok] =
           make_uint4(__byte_perm(v[p], v[p + 8], 0x5410), __byte_perm(v[16 + p], v[24 + p], 0x5410),
                      __byte_perm(v[p], v[p + 8], 0x7632), __byte_perm(v[16 + p], v[24 + p], 0x7632));
   }
+}
+
+// a / c for a < 2^20 by the reciprocal of c; the half keeps the result off the edges.
+__device__ __forceinline__ int part_of(int a, float inv) { return (int)(((float)a + 0.5f) * inv); }
+// First tile of CTA b where each of `ctas` has `each` and `extra` of them, evenly spread, one more. (All of these
+// side by side crowd their GPCs: a 4096 x 12288 down product of two experts took 20.5 us so, 16 spread.)
+__device__ __forceinline__ int first_tile(int b, int ctas, int each, int extra) {
+  return b * each + part_of(b * extra, __fdividef(1.f, (float)ctas));
 }
 
 // ---- the product --------------------------------------------------------------------------------------
@@ -403,11 +409,17 @@ struct Product {
 
   __device__ __forceinline__ void set_rows(const Mat& M, const Map& R) {
     const int lane = threadIdx.x & 31;
-    const int64_t o = (int64_t)lt * R.step, last = (int64_t)R.limit - 1;
-    auto row = [&](int r) { return r < 8 ? R.first + min(o + r, last) : R.second + min(o + R.ahead + r - 8, last); };
+    const int64_t o = (int64_t)lt * R.step, first = R.first + o, second = R.second + o;
+    const int last = (int)min((int64_t)R.limit - 1 - o, (int64_t)64);  // rows of the tile that are there, less one
+    const uint8_t* c = M.codes + 16 * (lane & 7);
+    const uint8_t *a = c + first * M.cstride, *b = c + second * M.cstride;
 #pragma unroll
-    for (int i = 0; i < 4; i++) pc[i] = M.codes + row((lane >> 3) + 4 * i) * M.cstride + 16 * (lane & 7);
-    ps = M.scales + row(L == TERN_T3_5PB_G128 ? lane >> 1 : lane & 15) * M.sstride;
+    for (int i = 0; i < 2; i++) {
+      pc[i] = a + min((lane >> 3) + 4 * i, last) * M.cstride;
+      pc[i + 2] = b + min((lane >> 3) + 4 * i + R.ahead, last) * M.cstride;
+    }
+    const int r = L == TERN_T3_5PB_G128 ? lane >> 1 : lane & 15;
+    ps = M.scales + (r < 8 ? first + min(r, last) : second + min(r - 8 + R.ahead, last)) * M.sstride;
   }
   // The block at the cursor into the ring stage at `stage`. Piece c of a row lies at (c / 2 ^ row % 4) * 32 +
   // c % 2 * 16, so that the four rows a half-warp reads 32 bytes of are in different banks.
@@ -553,7 +565,8 @@ struct Product {
     const uint32_t ring = ((sm100::smem_u32(tail) + 64 + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 127) & ~127u) + warp * (kDepth * kStage);
     const int blocks = (M.units + kBlk - 1) / kBlk;
     const int wk = min(s.wk, blocks);  // (M may be shorter than what was planned for)
-    const int kg = warp % wk, tg = warp / wk;
+    const float inv_wk = __fdividef(1.f, (float)wk), inv_tg = __fdividef(1.f, (float)s.tg);
+    const int tg = part_of(warp, inv_wk), kg = warp - tg * wk;
     kx = L == TERN_Q2_0_G128 ? 0xAAAAAAAAu : 85u;
     ky = 0x00500050u;
     asm volatile("" : "+r"(kx), "+r"(ky));
@@ -585,12 +598,12 @@ struct Product {
       const int b1 = min(t1, b0 + s.batch);
       int ta = b0, tb = b0;
       if (tg < s.tg) {
-        ta = b0 + (b1 - b0) * tg / s.tg;
-        tb = b0 + (b1 - b0) * (tg + 1) / s.tg;
+        ta = b0 + part_of((b1 - b0) * tg, inv_tg);
+        tb = b0 + part_of((b1 - b0) * (tg + 1), inv_tg);
       }
       for (int p0 = 0; p0 < blocks; p0 += s.pass) {
         const int p1 = min(blocks, p0 + s.pass);
-        const int lo = p0 + (p1 - p0) * kg / wk, hi = p0 + (p1 - p0) * (kg + 1) / wk;  // the warp's blocks
+        const int lo = p0 + part_of((p1 - p0) * kg, inv_wk), hi = p0 + part_of((p1 - p0) * (kg + 1), inv_wk);  // the warp's blocks
         int left = (tb - ta) * (hi - lo);  // blocks still to be copied
         const int total = left;
         lt = ta;
@@ -620,20 +633,53 @@ struct Product {
         if (fresh || s.pass < blocks) {
           __syncthreads();  // the operands of the pass before are no longer read (and the flags are clear)
           const int u0 = p0 * kBlk, nu = min(M.units, p1 * kBlk) - u0;
+          // (row or column tile, unit) pairs dealt to the warps, the next pair's activations under way meanwhile
+          const int all = (MODE == kInt8 ? tokens : NT) * nu;
           if constexpr (MODE == kInt8) {
+            constexpr int NE = T::kUnitK / 32;
+            float ahead[NE];
+            auto fetch = [&](int i) {
+#pragma unroll
+              for (int e = 0; e < NE; e++) ahead[e] = 0.f;
+              if (i < all) xs.template load<NE>(kRows == 1 || i < nu ? 0 : 1, (u0 + (i < nu ? i : i - nu)) * T::kUnitK + lane * NE, M.K, ahead);
+            };
+            static_assert(kRows <= 2, "");
+            fetch(warp);
 #pragma unroll 1
-            for (int t = 0; t < tokens; t++)
-#pragma unroll 1
-              for (int u = warp; u < nu; u += kMaxWarps)
-                build_int8<L>(xs, t, t % G::kTok, u0 + u, M.K, scr,
-                              reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes), odd + t);
+            for (int i = warp; i < all; i += kMaxWarps) {
+              float xv[NE];
+#pragma unroll
+              for (int e = 0; e < NE; e++) xv[e] = ahead[e];
+              fetch(i + kMaxWarps);
+              const int t = kRows == 1 || i < nu ? 0 : 1, u = i < nu ? i : i - nu;
+              build_int8<L>(xv, t % G::kTok, u0 + u, scr, reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes),
+                            odd + t);
+            }
           } else {
+            uint32_t ahead[kLaneWords<L>] = {};
+            auto split = [&](int i, int& n, int& u) {
+              n = 0;
+              u = i;
+#pragma unroll
+              for (int j = 1; j < NT; j++)
+                if (u >= nu) {
+                  u -= nu;
+                  n++;
+                }
+            };
+            int n, u;
+            split(warp, n, u);
+            if (warp < all) load_fp16<L>(xs, n * G::kTok, tokens, u0 + u, M.K, ahead);
 #pragma unroll 1
-            for (int n = 0; n < NT; n++)
-#pragma unroll 1
-              for (int u = warp; u < nu; u += kMaxWarps)
-                build_fp16<L>(xs, n * G::kTok, tokens, u0 + u, M.K,
-                              reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + n * G::kTileBytes));
+            for (int i = warp; i < all; i += kMaxWarps) {
+              uint32_t v[kLaneWords<L>];
+#pragma unroll
+              for (int e = 0; e < kLaneWords<L>; e++) v[e] = ahead[e];
+              const int n0 = n, v0 = u;
+              split(i + kMaxWarps, n, u);
+              if (i + kMaxWarps < all) load_fp16<L>(xs, n * G::kTok, tokens, u0 + u, M.K, ahead);
+              store_fp16<L>(v, n0 * G::kTok, tokens, u0 + v0, reinterpret_cast<uint4*>(frag + (size_t)v0 * kUnitBytes + n0 * G::kTileBytes));
+            }
           }
           __syncthreads();
         }
@@ -718,7 +764,7 @@ struct Product {
 
 // The cut for `tiles` tiles per CTA, `units` units of K and kRows rows of x within `room` bytes of shared
 // memory: as many blocks as fit beside the partial sums of a few tiles; then wk x tg warps so that the
-// busiest warp has the least to do, a tile's end counted as half a block. False when not even one block
+// busiest warp has the least to do, a tile's end counted as 0.3 of a block. False when not even one block
 // fits (never within the limits of the callers).
 template <class P>
 inline bool plan_split(int tiles, int units, size_t room, Split* out) {
@@ -738,7 +784,7 @@ inline bool plan_split(int tiles, int units, size_t room, Split* out) {
       const int passes = (blocks + s.pass - 1) / s.pass;
       s.pass = std::max(wk, (blocks + passes - 1) / passes);
       const int batches = (tiles + s.batch - 1) / s.batch;
-      const double work = (double)((s.batch + s.tg - 1) / s.tg) * ((s.pass + wk - 1) / wk + 0.5);
+      const double work = (double)((s.batch + s.tg - 1) / s.tg) * ((s.pass + wk - 1) / wk + 0.3);
       double cost = (double)batches * passes * (work + 1.0) + (passes > 1 ? 0.5 * batches * blocks : 0.0);
       // warps side by side along K read a row's bytes together; much less than 512 of them at a time cost DRAM
       // its open pages (24576 x 4096 Q2, one row: 13.6 us with 4, 8 or 16 warps along K, 14.2 with 2)
