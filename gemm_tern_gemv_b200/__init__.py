@@ -507,7 +507,7 @@ def linear(W: TernMatrix, x, bias=None, act: str = "none", gated: bool = False, 
     x = _operand(x, "x", lead + (W.k,), half, device)
     c = _layer_matrix(W, "W", device)
     if y is None:
-        y = x.new_empty(out)
+        y = x.new_empty(*out)  # (sizes one by one: a tuple takes longer to parse)
     else:
         _need(y, "y", out, half, device)
     b = r = z = None
@@ -552,12 +552,12 @@ def linear_backward(W: TernMatrix, dy, preact=None, act: str = "none", gated: bo
         raise ValueError(f"preact: needed for act {act!r} with gated={gated}")
     if identity and not need_dx and not need_dbias:
         return None, dy, None
-    dx = dy.new_empty((m, W.k)) if need_dx else None
-    db = dy.new_empty((n,), dtype=torch.float32) if need_dbias else None
+    dx = dy.new_empty(m, W.k) if need_dx else None
+    db = dy.new_empty(n, dtype=torch.float32) if need_dbias else None
     # rows of dz are 16-byte aligned: padded (and for act "none" a copy of dy) where n is not a multiple of 8
     own_dz = not identity or (need_dx and n % 8 != 0)
     stride = (n + 7) // 8 * 8 if own_dz else n
-    dz = dy.new_empty((m, stride)) if own_dz else dy
+    dz = dy.new_empty(m, stride) if own_dz else dy
     st = lib().tern_linear_backward(c, dy.data_ptr(), preact.data_ptr() if preact is not None else None, m, a,
                                     1 if gated else 0, dx.data_ptr() if need_dx else None, dz.data_ptr() if own_dz else None,
                                     stride, db.data_ptr() if need_dbias else None, _status_ptr(status, device),
@@ -600,7 +600,7 @@ def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str =
     router = _operand(router, "router", (router.shape[0], d), half, device)
     layer = _moe_layer(gate_up, down, router, top_k, act, renormalize, device)
     if y is None:
-        y = x.new_empty((tokens, d))
+        y = x.new_empty(tokens, d)
     else:
         _need(y, "y", (tokens, d), half, device)
     if residual is not None and residual is not y:
@@ -608,15 +608,15 @@ def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str =
     l = lib()
     if workspace is None:
         size = l.tern_moe_workspace_bytes(layer, tokens) or 1
-        workspace = x.new_empty((size,), dtype=torch.uint8)
+        workspace = x.new_empty(size, dtype=torch.uint8)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace: needs a contiguous tensor on {device}")
     else:
         size = workspace.numel() * workspace.element_size()
     weights = ids = wp = ip = None
     if return_routing:
-        weights = x.new_empty((tokens, max(0, top_k)), dtype=torch.float32)
-        ids = x.new_empty((tokens, max(0, top_k)), dtype=torch.int32)
+        weights = x.new_empty(tokens, max(0, top_k), dtype=torch.float32)
+        ids = x.new_empty(tokens, max(0, top_k), dtype=torch.int32)
         wp, ip = weights.data_ptr(), ids.data_ptr()
     st = l.tern_moe(layer, x.data_ptr(), tokens, residual.data_ptr() if residual is not None else None, y.data_ptr(), wp, ip,
                     workspace.data_ptr(), size, _raw_stream(torch, device))

@@ -2,16 +2,20 @@
 //   p = softmax(R x), the top_k experts of each token (ties to the lower index), optionally renormalised;
 //   y[t] = sum_j p[t][j] D_e (act(G_e x[t]) * U_e x[t]) (+ residual), e = ids[t][j].
 //
-// Bound by the packed weights of the experts in use, read once from HBM (and by latency for one token). Three
-// launches, each started while the one before ends (programmatic dependent launch):
+// The least is to read the packed weights of the experts in use once. What it takes is decoding: a segment of an
+// expert's pairs goes through the expert's weights as one product, so two segments decode them twice. 16 tokens,
+// 128 base-3 experts of 2048 x 768: 93 us (route 11, up 43, down 33, combine 3); 64 tokens, 8 Q2 experts of 4096 x
+// 12288: 297 us (up 170, down 115), of which the tensor cores are busy a third and shared memory two thirds; one
+// token, 8 of 64 Q2 experts of 2048 x 1024: 30 us, about as long as the launches take the host.
+// Four launches, each started while the one before ends (programmatic dependent launch):
 //   route  a cluster of eight CTAs for one to four tokens: each computes the logits of every eighth expert,
 //          the first collects them through the cluster's shared memory and picks.
 //   up     the (token, expert) pairs are sorted by expert; the 8-output tiles (gate and up rows) of all experts
 //          in use form one list that is dealt evenly to one CTA per SM. The products are those of
 //          tern_rows.cuh. h = act(g) u in fp32.
 //   down   the same over 16-row tiles of the down matrices, with h brought into fp16's range by a power of two
-//          per pair. Sums of a pair go to the workspace; whoever finishes a 16-column strip of y last (a counter
-//          per strip) adds its pairs up in the order of j, so the result does not depend on who that was.
+//          per pair, and over slices of K where f is long. Sums of a pair and slice go to the workspace.
+//   combine  adds a token's pairs up, in the order of j and of the slices.
 #include "tern_rows.cuh"
 
 namespace tern {
@@ -143,8 +147,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
 // share their registers): int8 digits for one or two tokens; fp16 column tiles for more, one of them, or two
 // where an expert gets six tokens or more on average. P::kRows pairs of an expert go through its weights
 // together.
-constexpr int kPlans = 8;  // cuts for up to 1, 2, 3, 4, 6, 8, 16 and any number of tiles
-__host__ __device__ constexpr int plan_tiles(int i) { return i < 4 ? i + 1 : i == 4 ? 6 : i == 5 ? 8 : i == 6 ? 16 : 32; }
+constexpr int kPlans = 9;  // cuts for up to 1, 2, 3, 4, 6, 8, 16, 32 and any number of tiles
+__host__ __device__ constexpr int plan_tiles(int i) { return i < 4 ? i + 1 : i == 4 ? 6 : i == 5 ? 8 : i == 6 ? 16 : i == 7 ? 32 : 128; }
 
 struct Lists {
   int segments, tiles;             // chunks of pairs; row tiles of all of them
@@ -428,7 +432,7 @@ int down_slices(int64_t f, int tokens, int top_k, int experts) {
     for (; s < 8; s++) {
       const int n = slice_blocks(blocks, s);
       rows::Split split;
-      if (P::plan(32, std::min(units, n * rows::kBlk), kRoom, &split) && split.pass >= n) break;
+      if (P::plan(128, std::min(units, n * rows::kBlk), kRoom, &split) && split.pass >= n) break;
     }
     const int n = slice_blocks(blocks, s);
     return (blocks + n - 1) / n;
