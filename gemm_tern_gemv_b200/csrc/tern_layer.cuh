@@ -23,12 +23,34 @@ struct Epilogue {
 __device__ __forceinline__ float h2f(uint16_t h) { return __half2float(__ushort_as_half(h)); }
 __device__ __forceinline__ uint16_t f2h(float f) { return __half_as_ushort(__float2half_rn(f)); }
 
-// gelu is z Phi(z) with Phi(z) = erfc(-z / sqrt 2) / 2 (no cancellation for negative z); its tanh form
-// is z sigmoid(u), u = sqrt(8 / pi) (z + 0.044715 z^3), since (1 + tanh(u / 2)) / 2 = sigmoid(u).
+// gelu is z Phi(z). For a = |z|, Phi(-a) = e^(-a^2 / 2) h(a), and h(a) = e^(a^2 / 2) Phi(-a) is smooth in t = 1 / (1 +
+// 0.3 a): a polynomial t P(t) of degree 8, fitted here by reweighted least squares of the relative error on [0, 16], is
+// within 2.2e-7 of it (5.3e-7 evaluated in fp32), so the negative tail keeps its relative precision too. The same
+// exponential gives Phi'. (With the library's erfc and exponential dz of 2048 x 12288 took 139 us, 53 so.)
+// Its tanh form is z sigmoid(u), u = sqrt(8 / pi) (z + 0.044715 z^3), since (1 + tanh(u / 2)) / 2 = sigmoid(u).
 __device__ __forceinline__ float gelu_tanh_u(float z) { return 1.5957691216057308f * (z + 0.044715f * z * z * z); }
 
+// Phi(z); *e is e^(-z^2 / 2).
+__device__ __forceinline__ float normal_cdf(float z, float* e) {
+  const float t = __fdividef(1.f, fmaf(0.3f, fabsf(z), 1.f));
+  float p = 0.034704924f;
+  p = fmaf(p, t, -0.15318732f);
+  p = fmaf(p, t, 0.19948818f);
+  p = fmaf(p, t, -0.04742666f);
+  p = fmaf(p, t, 0.12529191f);
+  p = fmaf(p, t, 0.10088924f);
+  p = fmaf(p, t, 0.12060054f);
+  p = fmaf(p, t, 0.11963908f);
+  *e = __expf(-0.5f * z * z);
+  const float q = p * t * *e;
+  return z < 0.f ? q : 1.f - q;
+}
+
 // Out of line: inlined many times over it would cost the epilogues their registers.
-static __device__ __noinline__ float gelu_erf(float z) { return 0.5f * z * erfcf(-0.70710678118654752f * z); }
+static __device__ __noinline__ float gelu(float z) {
+  float e;
+  return z * normal_cdf(z, &e);
+}
 
 __device__ __forceinline__ float act_fwd(int act, float z) {
   switch (act) {
@@ -36,27 +58,8 @@ __device__ __forceinline__ float act_fwd(int act, float z) {
     case TERN_ACT_RELU2: return z < 0.f ? 0.f : z * z;
     case TERN_ACT_SILU:
     case TERN_ACT_GELU_TANH: return __fdividef(z, 1.f + __expf(act == TERN_ACT_SILU ? -z : -gelu_tanh_u(z)));
-    case TERN_ACT_GELU: return gelu_erf(z);
+    case TERN_ACT_GELU: return gelu(z);
     default: return z;
-  }
-}
-
-// act'(z). The sigmoid's complement is taken as 1 / (1 + e^u), not 1 - sigmoid(u), so that the tails
-// keep their relative precision.
-__device__ __forceinline__ float act_bwd(int act, float z) {
-  switch (act) {
-    case TERN_ACT_RELU: return z > 0.f ? 1.f : (z <= 0.f ? 0.f : z);  // 0 at 0; NaN stays NaN
-    case TERN_ACT_RELU2: return z > 0.f ? 2.f * z : (z <= 0.f ? 0.f : z);
-    case TERN_ACT_SILU: {
-      const float s = 1.f / (1.f + expf(-z)), c = 1.f / (1.f + expf(z));
-      return s + z * s * c;
-    }
-    case TERN_ACT_GELU: return 0.5f * erfcf(-0.70710678118654752f * z) + 0.39894228040143268f * z * expf(-0.5f * z * z);
-    case TERN_ACT_GELU_TANH: {
-      const float u = gelu_tanh_u(z), s = 1.f / (1.f + expf(-u)), c = 1.f / (1.f + expf(u));
-      return s + z * s * c * 1.5957691216057308f * (1.f + 0.134145f * z * z);
-    }
-    default: return 1.f;
   }
 }
 
@@ -65,14 +68,21 @@ __device__ __forceinline__ float act_bwd(int act, float z) {
 __device__ __forceinline__ void act_both(int act, float z, float* f, float* df) {
   if (act == TERN_ACT_SILU || act == TERN_ACT_GELU_TANH) {
     const float u = act == TERN_ACT_SILU ? z : gelu_tanh_u(z);
-    // sigmoid s = 1 / (1 + e^-u) and its complement e^-u s; past e^80 both products with z vanish in fp32 alike
+    // sigmoid s = 1 / (1 + e^-u) and its complement e^-u s (not 1 - s: the tails keep their relative precision);
+    // past e^80 both products with z vanish in fp32 alike
     const float e = __expf(fminf(-u, 80.f)), s = __fdividef(1.f, 1.f + e), c = e * s;
     const float du = act == TERN_ACT_SILU ? 1.f : 1.5957691216057308f * (1.f + 0.134145f * z * z);
     *f = z * s;
     *df = s + z * s * c * du;
+  } else if (act == TERN_ACT_GELU) {
+    float e;
+    const float c = normal_cdf(z, &e);
+    *f = z * c;
+    *df = fmaf(0.39894228040143268f * z, e, c);
   } else {
     *f = act_fwd(act, z);
-    *df = act_bwd(act, z);
+    // relu's is 0 at 0; NaN stays NaN
+    *df = act == TERN_ACT_NONE ? 1.f : z > 0.f ? (act == TERN_ACT_RELU ? 1.f : 2.f * z) : (z <= 0.f ? 0.f : z);
   }
 }
 

@@ -10,7 +10,7 @@
 namespace tern {
 namespace {
 
-constexpr int kWarps = 8, kLanes = 16, kRowsAtOnce = kWarps * 32 / kLanes;
+constexpr int kPerSm = 4, kWarps = 8, kLanes = 16, kRowsAtOnce = kWarps * 32 / kLanes;
 
 struct DzParams {
   const uint16_t *dy, *z;
@@ -56,7 +56,7 @@ __device__ __forceinline__ float ld_peer(const float* local, uint32_t rank) {
 
 template <int VEC>
 __device__ __forceinline__ void dz_rows(const DzParams& p, int act, int64_t c, int64_t t0, int64_t t1, float (&s0)[VEC], float (&s1)[VEC]) {
-#pragma unroll 2
+#pragma unroll 1
   for (int64_t t = t0; t < t1; t += kRowsAtOnce) {
     const Halves<VEC> d = load_halves<VEC>(p.dy + t * p.nout + c);
     Halves<VEC> a{}, u{}, o0, o1;
@@ -81,7 +81,7 @@ __device__ __forceinline__ void dz_rows(const DzParams& p, int act, int64_t c, i
 }
 
 template <int VEC>
-__global__ void __launch_bounds__(kWarps * 32, 3) dz_kernel(const __grid_constant__ DzParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kPerSm) dz_kernel(const __grid_constant__ DzParams p) {
   constexpr int kCols = kLanes * VEC;
   __shared__ float sums[2][kRowsAtOnce][kCols];
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
@@ -118,7 +118,12 @@ template <int VEC>
 cudaError_t launch_dz(const DzParams& p, cudaStream_t st) {
   const int64_t cols = kLanes * VEC;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)((p.nout + cols - 1) / cols), p.m >= 64 ? 8 : p.m >= 16 ? 2 : 1);
+  const int64_t blocks = (p.nout + cols - 1) / cols;
+  // as many slices of the rows (1, 2, 4 or 8 to a cluster) as still run at the same time: 2048 x 24576 gated takes 60 us
+  // with 8, 52 with 4; 65 with 6, which leave SMs of the GPCs over
+  int slices = p.m >= 64 ? 8 : p.m >= 16 ? 2 : 1;
+  while (slices > 1 && blocks * slices > kPerSm * sm_count()) slices /= 2;
+  cfg.gridDim = dim3((unsigned)blocks, (unsigned)slices);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
