@@ -144,9 +144,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
 
 // ---- the experts ------------------------------------------------------------------------------------------
 // The form of the product is the same for all experts of a call (side by side in one kernel the forms would
-// share their registers): int8 digits for one or two tokens; fp16 column tiles for more, one of them, or two
-// where an expert gets six tokens or more on average. P::kRows pairs of an expert go through its weights
-// together.
+// share their registers): int8 digits or fp16 column tiles, see with_form. P::kRows pairs of an expert go through
+// its weights together.
 constexpr int kPlans = 9;  // cuts for up to 1, 2, 3, 4, 6, 8, 16, 32 and any number of tiles
 __host__ __device__ constexpr int plan_tiles(int i) { return i < 4 ? i + 1 : i == 4 ? 6 : i == 5 ? 8 : i == 6 ? 16 : i == 7 ? 32 : 128; }
 
@@ -405,13 +404,19 @@ cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t s
   return launch(kern, sm_count(), rows::kThreads, smem, st, &q);
 }
 
-// f(form) with the form of the product that a call takes.
+// f(form) with the form of the product that a call takes: int8 digits for few pairs per expert (on average), else
+// fp16 column tiles. The int8 form decodes faster, but an expert of more than P::kRows pairs (Q2 two, else one) takes
+// it again for the next; 64 experts of 2048 x 1024, 8 chosen, us with int8 and with fp16:
+//   pairs per expert   1/2        1          2                    1/2        1          2                 1          2
+//   Q2                 43 / 46    53 / 57    68 / 66    base-3    53 / 57    71 / 73    109 / 87    binary  52 / 70    71 / 83
+// (base-3 with 128 experts of 2048 x 768 and one pair: 95 / 92). Six pairs or more on average take two column tiles.
 template <class P> struct Form { using type = P; };
 template <int L, class F>
 auto with_form(int tokens, int top_k, int experts, F f) {
-  if (tokens == 1) return f(Form<rows::Product<L, rows::kInt8, 1>>{});
-  if (tokens == 2) return f(Form<rows::Product<L, rows::kInt8, 2 / rows::Geo<L, rows::kInt8>::kTok>>{});
-  if (tokens * top_k < 6 * experts) return f(Form<rows::Product<L, rows::kFp16, 1>>{});
+  const int pairs = tokens * top_k;
+  const int few = L == TERN_Q1_0_G128 ? 2 * experts : L == TERN_Q2_0_G128 ? experts : experts - 1;
+  if (tokens == 1 || pairs <= few) return f(Form<rows::Product<L, rows::kInt8, 1>>{});
+  if (pairs < 6 * experts) return f(Form<rows::Product<L, rows::kFp16, 1>>{});
   return f(Form<rows::Product<L, rows::kFp16, 2>>{});
 }
 

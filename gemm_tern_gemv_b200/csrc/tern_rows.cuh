@@ -7,7 +7,7 @@
 // shared memory (cp.async, four whole lines an instruction; the copies need no registers and no barrier
 // but the warp's own). A unit lies in one 128-weight group (Q2) or two (slots 0 and 1 of base-3 and binary).
 // Two forms of the product:
-//   int8 (1-2 rows of x per tile of 8 MMA columns): activations become exact integers. Per unit, slot
+//   int8 (one row of x, two rows of 8 MMA columns at most): activations become exact integers. Per unit, slot
 //     and row of x, X = round(x 2^S) with S from the largest |x| of the slot, written as four balanced
 //     base-256 digits; the columns are (row of x, or slot) x (digit), and the epilogue joins them. The
 //     codes become u8 operands with one LOP3 per four weights and no shift to a common place:
