@@ -4,7 +4,7 @@
 //
 // The least is to read the packed weights of the experts in use once. What it takes is decoding: a segment of an
 // expert's pairs goes through the expert's weights as one product, so two segments decode them twice. 16 tokens,
-// 128 base-3 experts of 2048 x 768: 93 us (route 11, up 43, down 33, combine 3); 64 tokens, 8 Q2 experts of 4096 x
+// 128 base-3 experts of 2048 x 768: 92 us (route 11, up 43, down 33, combine 3); 64 tokens, 8 Q2 experts of 4096 x
 // 12288: 297 us (up 170, down 115), of which the tensor cores are busy a third and shared memory two thirds; one
 // token, 8 of 64 Q2 experts of 2048 x 1024: 30 us, about as long as the launches take the host.
 // Four launches, each started while the one before ends (programmatic dependent launch):
@@ -149,6 +149,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
 constexpr int kPlans = 9;  // cuts for up to 1, 2, 3, 4, 6, 8, 16, 32 and any number of tiles
 __host__ __device__ constexpr int plan_tiles(int i) { return i < 4 ? i + 1 : i == 4 ? 6 : i == 5 ? 8 : i == 6 ? 16 : i == 7 ? 32 : 128; }
 
+constexpr int kMaxRows = 16;  // pairs that go through an expert's weights together, at most
+
 struct Lists {
   int segments, tiles;             // chunks of pairs; row tiles of all of them
   uint16_t pair[kMaxPairs];        // pairs sorted by expert
@@ -157,9 +159,9 @@ struct Lists {
   uint8_t seg_count[kMaxPairs];
   int count[kMoeMaxExperts], first[kMoeMaxExperts];
   uint32_t total[kMoeMaxExperts / 32];
-  int index[16];                   // rows of the activations of the current segment
-  float mul[16];                   // and their powers of two
-  uint32_t top[16];                // largest |h| of each in this CTA
+  int index[kMaxRows];             // rows of the activations of the current segment
+  float mul[kMaxRows];             // and their powers of two
+  uint32_t top[kMaxRows];          // largest |h| of each in this CTA
 };
 
 // Sorts the pairs by expert, in their own order within it (every CTA has to cut the same segments), and cuts
@@ -262,6 +264,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_up_kernel(const __grid_
   __shared__ Lists s;
   const MoeParams& p = q.p;
   constexpr int kStep = P::kTileRows / 2;
+  static_assert(P::kRows <= kMaxRows);
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int per = p.f / kStep;  // tiles of a segment
@@ -298,6 +301,7 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
   __shared__ Lists s;
   const MoeParams& p = q.p;
   constexpr int kStep = P::kTileRows;
+  static_assert(P::kRows <= kMaxRows);
   sm100::griddep_launch_dependents();
   sm100::griddep_wait();
   const int per = p.d / kStep, tid = threadIdx.x;
@@ -409,14 +413,19 @@ cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t s
 // it again for the next; 64 experts of 2048 x 1024, 8 chosen, us with int8 and with fp16:
 //   pairs per expert   1/2        1          2                    1/2        1          2                 1          2
 //   Q2                 43 / 46    53 / 57    68 / 66    base-3    53 / 57    71 / 73    109 / 87    binary  52 / 70    71 / 83
-// (base-3 with 128 experts of 2048 x 768 and one pair: 95 / 92). Six pairs or more on average take two column tiles.
+// (base-3 with 128 experts of 2048 x 768 and one pair: 95 / 92). Two column tiles where an expert's pairs often need
+// them; eight experts of 4096 x 12288, 2 chosen, us with one and with two:
+//   pairs per expert   4            8            16
+//   Q2                 153 / 206    193 / 218    302 / 297
+//   base-3             245 / 238    387 / 342    680 / 529
+//   binary             212 / 199    343 / 276    591 / 448
 template <class P> struct Form { using type = P; };
 template <int L, class F>
 auto with_form(int tokens, int top_k, int experts, F f) {
   const int pairs = tokens * top_k;
   const int few = L == TERN_Q1_0_G128 ? 2 * experts : L == TERN_Q2_0_G128 ? experts : experts - 1;
   if (tokens == 1 || pairs <= few) return f(Form<rows::Product<L, rows::kInt8, 1>>{});
-  if (pairs < 6 * experts) return f(Form<rows::Product<L, rows::kFp16, 1>>{});
+  if (pairs < (L == TERN_Q2_0_G128 ? 14 : 4) * experts) return f(Form<rows::Product<L, rows::kFp16, 1>>{});
   return f(Form<rows::Product<L, rows::kFp16, 2>>{});
 }
 
