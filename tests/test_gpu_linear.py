@@ -328,3 +328,37 @@ def test_shared_sums_repeat_in_graphs(m):
         graph.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(y, want) for y in ys)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("n,m", [(2500, 1), (9700, 1), (9700, 2)])
+def test_one_and_two_rows_on_many_outputs(layout, n, m):
+    # large matrices take other forms of the product than small ones
+    _check(layout, m, n, 640, act="silu", bias=True, residual=True, preact=True)
+    _check(layout, m, 2 * n, 1152, act="gelu", gated=True)
+    k = 384
+    codes, s, w = weights(layout, n, k, 80)
+    W = _matrix(codes, s, layout, k)
+    x = half(81, m, k, scale=1e-2)
+    x[np.arange(m), np.arange(m) * 37 + 5] = 60000.0  # one huge activation beside tiny ones
+    check(T.linear(W, _dev(x)).cpu().numpy(), L.linear(w, f64(x)), L.linear_bound(w, f64(x)), "wide range")
+    x = half(82, m, k)
+    x[0, 5] = np.inf
+    if m > 1:
+        x[1, k - 1] = np.nan
+    y = T.linear(W, _dev(x)).cpu().numpy().astype(np.float64)
+    with np.errstate(invalid="ignore"):
+        want = np.stack([(f64(x)[i] * w).sum(1) for i in range(m)])
+    assert np.array_equal(np.isnan(y), np.isnan(want)) and np.array_equal(y[np.isinf(want)], want[np.isinf(want)])
+    codes, s, w = weights(layout, n, k, 83, scale=1.0)
+    x = np.random.default_rng(84).integers(-1, 2, size=(m, k)).astype(np.float16)
+    y = T.linear(_matrix(codes, s, layout, k), _dev(x)).cpu().numpy()
+    assert np.array_equal(y.astype(np.float64), f64(x) @ w.T)
+    # scales whose double does not fit fp16 and subnormal ones
+    s[:] = np.float16(2.0 ** -16)
+    s[7, 0], s[n - 1, 2], s[n // 2, 1], s[20, 1] = 65504.0, -33000.0, 40000.0, np.float16(2.0 ** -24)
+    w = np.sign(w) * np.repeat(s.astype(np.float64), 128, axis=1)
+    x = half(85, m, k, scale=2.0 ** -10)
+    y, want = T.linear(_matrix(codes, s, layout, k), _dev(x)).cpu().numpy(), L.linear(w, f64(x))
+    fits = np.abs(want) < 65000
+    check(np.where(fits, y, 0), np.where(fits, want, 0), L.linear_bound(w, f64(x)), "extreme scales")

@@ -166,3 +166,27 @@ def test_refused_operands():
 def test_long_down_rows(layout, tokens, f):
     # down products whose K is cut into slices
     Layer(layout, 128, f, 2, seed=15).check(half(11, tokens, 128), 1, residual=half(12, tokens, 128))
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("tokens,experts,top_k", [(2, 3, 3), (5, 40, 8), (16, 16, 2), (40, 64, 2), (64, 200, 4), (9, 8, 4), (30, 6, 3)])
+def test_pairs_per_expert(layout, tokens, experts, top_k):
+    # from less than one pair for each expert to fifteen: every form of the product, and experts of many pairs in each
+    lay = Layer(layout, 256, 384, experts, seed=60)
+    x = half(tokens, tokens, 256)
+    lay.check(x, top_k, residual=half(9, tokens, 256))
+    lay.r[:] *= np.float16(0)
+    lay.r[0] = 1  # one expert is taken by every token with a positive sum, the others by index
+    lay.check(x, top_k)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_infinite_activations_of_some_tokens(layout):
+    # pairs of tokens with and without infinities in the same experts
+    lay = Layer(layout, 256, 384, 24, seed=61)
+    x = half(62, 12, 256)
+    want = T.moe(lay.G, lay.D, _dev(lay.r), _dev(x), 2)
+    x[3, 7], x[8, 0] = np.inf, np.nan
+    got = T.moe(lay.G, lay.D, _dev(lay.r), _dev(x), 2)
+    rest = [i for i in range(12) if i not in (3, 8)]
+    assert torch.equal(got[rest], want[rest]) and not torch.isfinite(got[[3, 8]]).all(1).any()
