@@ -365,15 +365,14 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   for (int i = threadIdx.x; i < kBigTiles * BM; i += kThreads) big[i] = 0;
   if (warp == 0 && lane == 0) { prefetch_tmap(&tmap_x); prefetch_tmap(&tmap_w); }
   if (LAYOUT == TERN_T3_5PB_G128) {
-    for (int i = threadIdx.x; i < 256 * 32; i += kThreads) {
-      const int v = i / 32;
-      uint32_t f = 0, r = (uint32_t)v;
-      if (v < 243) {
+    // a thread computes one entry and stores a third of its copies, a warp's in different banks at a time
+    const int v = threadIdx.x % 256;
+    uint32_t f = 0, r = (uint32_t)v;
+    if (v < 243) {
 #pragma unroll
-        for (int d = 0; d < 5; d++) { f |= ((r % 3u + 3u) & 3u) << (2 * d); r /= 3u; }  // c - 1 as two bits
-      }
-      lut[i] = f;  // an invalid byte reads as five t = 0
-    }
+      for (int d = 0; d < 5; d++) { f |= ((r % 3u + 3u) & 3u) << (2 * d); r /= 3u; }  // c - 1 as two bits
+    }  // an invalid byte reads as five t = 0
+    for (int i = threadIdx.x / 256; i < 32; i += kThreads / 256) lut[v * 32 + ((v + i) & 31)] = f;
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kTmemCols);
