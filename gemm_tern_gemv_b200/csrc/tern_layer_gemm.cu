@@ -354,6 +354,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   const bool gated = !TRANS && p.e.gated;
   const int step = gated ? 64 : BM;  // outputs of a tile
 
+  griddep_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < STAGES; i++) { mbar_init(full + i, 2); mbar_init(empty + i, 1); }
     for (int i = 0; i < ASTAGES; i++) { mbar_init(dfull + i, 8); mbar_init(dempty + i, 1); }
@@ -382,6 +383,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are ready before either arrives on the other's
   tc_fence_after();
+  griddep_wait();  // from here on operands are read and results written
   const uint32_t tmem = __reduce_or_sync(0xffffffffu, *tmem_holder);  // the same in all lanes, in a uniform register
 
   if (warp == 0 || warp == 2) {
@@ -719,8 +721,10 @@ cudaLaunchConfig_t config(int clusters, int splits, cudaStream_t st, cudaLaunchA
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)(2 * splits);
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cfg;
 }
 
@@ -735,8 +739,9 @@ int clusters_at_once(int splits) {
       const void* kern = reinterpret_cast<const void*>(&layer_gemm_kernel<LAYOUT, TRANS>);
       if (allow_smem(kern, SMEM_BYTES) != cudaSuccess) return;
       for (int i = 1; i <= kMaxSplits; i++) {
-        cudaLaunchAttribute attr[1];
+        cudaLaunchAttribute attr[2];
         cudaLaunchConfig_t cfg = config(1, i, nullptr, attr);
+        cfg.numAttrs = 1;  // the cluster
         if (cudaOccupancyMaxActiveClusters(&of[i], kern, &cfg) != cudaSuccess) {
           of[i] = 0;
           (void)cudaGetLastError();
@@ -797,7 +802,7 @@ cudaError_t launch_t(const tern_matrix& W, const uint16_t* x, int64_t xstride, P
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)p.rtiles + 1) / 2 * p.mtiles;
   const int64_t clusters = p.splits > 1 ? tiles : std::min<int64_t>(tiles, sm_count() / 2);
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   cudaLaunchConfig_t cfg = config((int)clusters, p.splits, st, attr);
   return cudaLaunchKernelEx(&cfg, &layer_gemm_kernel<LAYOUT, TRANS>, mx, mw, (const Params)p);
 }

@@ -6,6 +6,7 @@
 // (16 bytes where rows are aligned to that). Column sums stay in fp32 registers, are joined over the warps
 // through shared memory and over the row slices through the cluster's shared memory, always in the same
 // order. dx is the transposed product of tern_layer_gemm.cu on the rounded dz.
+#include "sm100.cuh"
 #include "tern_layer.cuh"
 
 namespace tern {
@@ -85,6 +86,8 @@ template <int VEC>
 __global__ void __launch_bounds__(kWarps * 32, kPerSm) dz_kernel(const __grid_constant__ DzParams p) {
   constexpr int kCols = kLanes * VEC;
   __shared__ float sums[2][kRowsAtOnce][kCols];
+  sm100::griddep_launch_dependents();
+  sm100::griddep_wait();
   const int lane = threadIdx.x % kLanes, sub = threadIdx.x / kLanes;
   const int64_t c = (int64_t)blockIdx.x * kCols + lane * VEC;
   const int64_t r0 = p.m * blockIdx.y / gridDim.y, r1 = p.m * (blockIdx.y + 1) / gridDim.y;
@@ -127,13 +130,15 @@ cudaError_t launch_dz(const DzParams& p, cudaStream_t st) {
   cfg.gridDim = dim3((unsigned)blocks, (unsigned)slices);
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 1;
   attr[0].val.clusterDim.y = cfg.gridDim.y;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, dz_kernel<VEC>, p);
 }
 
