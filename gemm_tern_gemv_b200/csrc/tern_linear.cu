@@ -1,6 +1,6 @@
 // Fused linear layer y = act(W x + b) (+ residual), gated or not, on packed ternary weights.
 //
-// Few rows of x (up to kFewRows): linear_rows_kernel, the register core of tern_rows.cuh. One CTA per SM
+// Few rows of x (see few_rows): linear_rows_kernel, the register core of tern_rows.cuh. One CTA per SM
 // owns a run of 16-row tiles (gated: 8 gate rows and their 8 up rows, so that both halves of an output meet
 // in one thread); its warps cut K, their partial sums meet in shared memory in warp order, and the epilogue
 // runs on the fp32 sums.
@@ -102,14 +102,20 @@ cudaError_t pick_rows(RowsParams& p, cudaStream_t st) {
   return launch_rows<L, rows::Product<L, rows::kFp16, 4>>(p, st);
 }
 
-constexpr int kFewRows = 16;
+// Rows of x that the register core takes. Above eight rows the operands of base-3 and binary (four column tiles, half
+// of them zeros) stop fitting into shared memory at about k = 5120 and are built again for every few tiles: 16 rows x
+// 4096 x 12288 took 45 us base-3 and 37 binary, against 32 and 26 on the tensor cores of the other kernel; x 4096 x 4096
+// 17.6 and 13.5 against 19.2 and 16.7.
+bool few_rows(const tern_matrix& W, int64_t m) {
+  return m <= 8 || (m <= 16 && (W.layout == TERN_Q2_0_G128 || W.k <= 5120));
+}
 
 }  // namespace
 
 cudaError_t launch_linear(const tern_matrix& W, const uint16_t* x, int64_t m, uint16_t* y, const Epilogue& e,
                           uint32_t flags, uint32_t* status, cudaStream_t st) {
   const int64_t nout = e.gated ? W.n / 2 : W.n;
-  if (m <= kFewRows) {
+  if (few_rows(W, m)) {
     RowsParams p{};
     p.mat = rows::Mat{static_cast<const uint8_t*>(W.codes), W.scales, W.code_row_stride, W.scale_row_stride, (int)W.k,
                       (int)row_bytes(W.layout, W.k), (int)(W.k / kGroup), (int)((row_bytes(W.layout, W.k) + 31) / 32)};
