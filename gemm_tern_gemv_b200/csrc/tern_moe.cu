@@ -29,9 +29,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void store_first(double* local, double v) {  // into the first CTA's copy of *local
   uint32_t remote;
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(remote) : "r"(sm100::smem_u32(local)));
@@ -64,7 +63,9 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
   const int t0 = (int)(blockIdx.x / kRouteCtas) * TOK;
   const int rank = (int)cluster_rank();
   sm100::griddep_launch_dependents();
+  cluster_arrive();
   sm100::griddep_wait();
+  bool met = false;  // the first CTA is known to run, so that its shared memory may be written
   for (int i = (int)(blockIdx.x * kRouteThreads + threadIdx.x); i < p.tokens * p.top_k; i += (int)gridDim.x * kRouteThreads)
     p.clear[i] = 0;  // largest |h| of each pair
   for (int i = rank + kRouteCtas * warp; i < p.experts * parts; i += kWarps) {
@@ -88,6 +89,8 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
         }
       }
     }
+    if (!met) cluster_wait();
+    met = true;
 #pragma unroll
     for (int k = 0; k < TOK; k++) {
       double v = (s[k][0] + s[k][1]) + (s[k][2] + s[k][3]);
@@ -95,7 +98,9 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
       if (lane == 0) store_first(&logit[k][i], v);
     }
   }
-  cluster_sync();
+  if (!met) cluster_wait();
+  cluster_arrive();
+  cluster_wait();
   if (rank || warp >= TOK || t0 + warp >= p.tokens) return;
   if (parts > 1) {  // the parts' sums in their order; at most 64 of them, read before any is overwritten
     double v = 0.;
