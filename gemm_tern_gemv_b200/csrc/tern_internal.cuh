@@ -142,6 +142,7 @@ struct MoeParams {
   uint32_t* clear;           // largest |h| of each (token, expert) pair as bits
   float *h, *z;              // [tokens * top_k][f] expert activations, [slices][tokens * top_k][d] down products
   int slices;                // of the down products' K
+  int scaled;                // the down products take h as fp16 times a power of two: `clear` is needed
   int tokens, d, f, experts, top_k, act, renormalize;
 };
 struct MoePlan {  // workspace offsets

@@ -148,7 +148,7 @@ __global__ void __cluster_dims__(kRouteCtas, 1, 1) __launch_bounds__(kRouteThrea
 }
 
 // ---- the experts ------------------------------------------------------------------------------------------
-// The form of the product is the same for all experts of a call (side by side in one kernel the forms would
+// The form of a product (gate/up or down) is the same for all experts of a call (side by side in one kernel the forms would
 // share their registers): int8 digits or fp16 column tiles, see with_form. P::kRows pairs of an expert go through
 // its weights together.
 constexpr int kPlans = 9;  // cuts for up to 1, 2, 3, 4, 6, 8, 16, 32 and any number of tiles
@@ -291,10 +291,10 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_up_kernel(const __grid_
                const float h = act_fwd(p.act, gate) * up;
                p.h[(int64_t)pair[c] * p.f + tile * kStep + r] = h;
                // largest |h| of the pair, as bits: order does not matter to a maximum. NaN counts as the largest.
-               if (P::kMode == rows::kFp16) atomicMax(s.top + c, __float_as_uint(h) & 0x7fffffffu);
+               if (p.scaled) atomicMax(s.top + c, __float_as_uint(h) & 0x7fffffffu);
              });
     __syncthreads();
-    if (P::kMode == rows::kFp16 && (int)threadIdx.x < n) atomicMax(p.clear + pair[threadIdx.x], s.top[threadIdx.x]);
+    if (p.scaled && (int)threadIdx.x < n) atomicMax(p.clear + pair[threadIdx.x], s.top[threadIdx.x]);
     __syncthreads();
     t += b - a;
   }
@@ -458,6 +458,11 @@ int down_slices(int64_t f, int tokens, int top_k, int experts) {
   });
 }
 
+template <int L>
+bool takes_fp16(const MoeParams& p) {
+  return with_form<L>(p.tokens, p.top_k, p.experts, [](auto form) { return decltype(form)::type::kMode == rows::kFp16; });
+}
+
 template <bool UP>
 cudaError_t dispatch(const tern_matrix& W, const MoeParams& p, cudaStream_t st) {
   switch (W.layout) {
@@ -495,6 +500,10 @@ cudaError_t launch_moe(const tern_matrix& G, const tern_matrix& D, MoeParams p, 
   p.h = reinterpret_cast<float*>(ws + w.h);
   p.z = reinterpret_cast<float*>(ws + w.z);
   p.slices = w.slices;
+  // (the layouts, and with them the forms of the two products, may differ)
+  p.scaled = D.layout == TERN_Q2_0_G128     ? takes_fp16<TERN_Q2_0_G128>(p)
+             : D.layout == TERN_T3_5PB_G128 ? takes_fp16<TERN_T3_5PB_G128>(p)
+                                            : takes_fp16<TERN_Q1_0_G128>(p);
   const int tok = p.tokens > 32 ? 4 : p.tokens > 16 ? 2 : 1;
   const void* route = tok == 4   ? reinterpret_cast<const void*>(&route_kernel<4>)
                       : tok == 2 ? reinterpret_cast<const void*>(&route_kernel<2>)

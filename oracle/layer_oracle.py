@@ -100,15 +100,18 @@ def moe(gate_up, down, router, x, top_k, name="silu", renormalize=True, residual
 
 
 # ------------------------------------------------------------------------------------- error bounds
-def product_bound(w, x):
+def product_bound(w, x, common=True):
     """Bound on a kernel's error of x w^T before rounding. Sums run in fp32: at most k / 16 + 64 dependent
     additions (tensor-core steps of 16, then the joining of partial sums), each off by at most one unit
-    (2^-23, tensor cores may truncate) of a partial sum no larger than A = sum |w x|. Where x is held as
-    integers with a common exponent for 128 of them, each x is off by at most 2^-25 of the largest."""
+    (2^-23, tensor cores may truncate) of a partial sum no larger than A = sum |w x|. `common`: where x is
+    held as integers with a common exponent for 128 of them, each x is off by at most 2^-25 of the largest."""
     k = x.shape[1]
     a = np.abs(x) @ np.abs(w).T
+    sums = 2.0 ** -23 * (k / 16 + 64) * a
+    if not common:
+        return sums
     top = np.repeat(np.abs(x).reshape(x.shape[0], k // GROUP, GROUP).max(2), GROUP, axis=1)
-    return 2.0 ** -23 * (k / 16 + 64) * a + 2.0 ** -25 * (top @ np.abs(w).T)
+    return sums + 2.0 ** -25 * (top @ np.abs(w).T)
 
 
 def _slope(name, z, dz):
@@ -116,11 +119,10 @@ def _slope(name, z, dz):
     return 2 * (np.maximum(z, 0) + dz) if name == "relu2" else np.full_like(z, 1.0 if name in ("none", "relu") else 1.13)
 
 
-def linear_bound(w, x, bias=None, name="none", gated=False, residual=None):
-    """Bound on |y - linear()| for an fp16 y: the product's error through the activation, 16 units of fp32
-    for evaluating activation, bias, gate and residual, and one rounding to fp16."""
+def _linear_error(w, x, bias=None, name="none", gated=False, residual=None, common=True):
+    """(y, bound on the error of y before its rounding): see linear_bound."""
     z = preact(w, x, bias)
-    dz = product_bound(w, x) + 2 * HALF_F32 * np.abs(z)
+    dz = product_bound(w, x, common) + 2 * HALF_F32 * np.abs(z)
     f = z.shape[1] // 2
     if gated:
         a, u = act(name, z[:, :f]), z[:, f:]
@@ -134,6 +136,13 @@ def linear_bound(w, x, bias=None, name="none", gated=False, residual=None):
     if residual is not None:
         y = y + residual
         err = err + 2 * HALF_F32 * (np.abs(y) + np.abs(residual))
+    return y, err
+
+
+def linear_bound(w, x, bias=None, name="none", gated=False, residual=None, common=True):
+    """Bound on |y - linear()| for an fp16 y: the product's error through the activation, 16 units of fp32
+    for evaluating activation, bias, gate and residual, and one rounding to fp16."""
+    y, err = _linear_error(w, x, bias, name, gated, residual, common)
     return err * (1 + HALF_F16) + HALF_F16 * np.abs(y) + TINY_F16
 
 
@@ -168,10 +177,13 @@ def backward_bounds(w, dy, z, name="none", gated=False):
     return b_dx * (1 + HALF_F16) + HALF_F16 * np.abs(dx) + TINY_F16, b_dz + TINY_F16, b_db
 
 
-def moe_bound(gate_up, down, router, x, top_k, name="silu", renormalize=True, residual=None):
+def moe_bound(gate_up, down, router, x, top_k, name="silu", renormalize=True, residual=None, held=None):
     """Bound on |y - moe()|: each expert's h = act(gate) * up with its bound as in linear_bound, rounded to
     at most 11 bits for the second product (2^-11 |h|, with 2^-24 of the largest h of the row where a
-    common exponent holds it), the product's sums, weights off by 16 units of fp32, one rounding."""
+    common exponent holds it), the product's sums, weights off by 16 units of fp32, one rounding.
+    `held` says how h comes to the second product and leaves out what that does not do: "fp16" (times a power of two
+    that brings the pair's largest to [2^14, 2^15): 2^-11 |h|, and 2^-25 of a scaled value, so 2^-39 of the largest)
+    or "integers" (2^-27 of the largest)."""
     weights, ids = route(x @ router.T, top_k, renormalize)
     y, _, _ = moe(gate_up, down, router, x, top_k, name, renormalize, residual)
     err = np.zeros_like(x)
@@ -180,7 +192,11 @@ def moe_bound(gate_up, down, router, x, top_k, name="silu", renormalize=True, re
             g, dn = gate_up[ids[t, j]], down[ids[t, j]]
             f = dn.shape[1]
             h = linear(g, x[t:t + 1], None, name, True)
-            eh = linear_bound(g, x[t:t + 1], None, name, True) + 2.0 ** -24 * np.abs(h).max()  # holds the 2^-11 |h|
+            if held is None:
+                eh = linear_bound(g, x[t:t + 1], None, name, True) + 2.0 ** -24 * np.abs(h).max()  # holds the 2^-11 |h|
+            else:
+                eh = _linear_error(g, x[t:t + 1], None, name, True, None, False)[1]
+                eh = eh * (1 + HALF_F16) + (HALF_F16 * np.abs(h) + 2.0 ** -39 * np.abs(h).max() if held == "fp16" else 2.0 ** -27 * np.abs(h).max())
             s = np.abs(h) @ np.abs(dn).T
             e = eh @ np.abs(dn).T + 2.0 ** -23 * (f / 16 + 64) * s
             err[t] += weights[t, j] * (e[0] + 18 * HALF_F32 * s[0])
