@@ -139,7 +139,7 @@ struct MoeParams {
   uint16_t* y;               // [tokens][d]
   float* weights;            // [tokens][top_k]
   int32_t* ids;              // [tokens][top_k]
-  uint32_t* clear;           // largest |h| of each (token, expert) pair as bits
+  uint32_t* clear;           // largest finite |h| of each (token, expert) pair as bits
   float *h, *z;              // [tokens * top_k][f] expert activations, [slices][tokens * top_k][d] down products
   int slices;                // of the down products' K
   int scaled;                // the down products take h as fp16 times a power of two: `clear` is needed

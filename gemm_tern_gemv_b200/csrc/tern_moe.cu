@@ -290,8 +290,9 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_up_kernel(const __grid_
              n, [] {}, [&](int tile, int r, int c, float gate, float up) {
                const float h = act_fwd(p.act, gate) * up;
                p.h[(int64_t)pair[c] * p.f + tile * kStep + r] = h;
-               // largest |h| of the pair, as bits: order does not matter to a maximum. NaN counts as the largest.
-               if (p.scaled) atomicMax(s.top + c, __float_as_uint(h) & 0x7fffffffu);
+               // largest finite |h| of the pair, as bits: order does not matter to a maximum
+               const uint32_t bits = __float_as_uint(h) & 0x7fffffffu;
+               if (p.scaled && bits < 0x7f800000u) atomicMax(s.top + c, bits);
              });
     __syncthreads();
     if (p.scaled && (int)threadIdx.x < n) atomicMax(p.clear + pair[threadIdx.x], s.top[threadIdx.x]);
@@ -321,9 +322,9 @@ __global__ void __launch_bounds__(rows::kThreads, 1) moe_down_kernel(const __gri
       const int pr = pair[tid];
       s.index[tid] = pr;
       if (P::kMode == rows::kFp16) {
-        // the fp16 form takes h times a power of two that brings the pair's largest to [2^14, 2^15)
+        // the fp16 form takes h times a power of two that brings the pair's largest finite one to [2^14, 2^15)
         const uint32_t top = p.clear[pr];
-        s.mul[tid] = top == 0 || top >= 0x7f800000u ? 1.f : rows::exp2i(min(100, 15 - rows::exponent(top)));
+        s.mul[tid] = top == 0 ? 1.f : rows::exp2i(min(100, 15 - rows::exponent(top)));
       }
     }
     __syncthreads();

@@ -42,3 +42,22 @@ def test_expert_activations_outside_fp16s_range(up, down, tokens, size):
     assert np.abs(h).max() > 1e5 if size == "large" else np.median(np.abs(h)[h != 0]) < 2.0 ** -24
     assert np.abs(want).max() < 6e4 and np.array_equal(ids.cpu().numpy(), wi)
     check(y.cpu().numpy(), want, L.moe_bound(*args, held="fp16"), f"up {up} down {down}, {tokens} tokens")
+
+
+@pytest.mark.parametrize("up", LAYOUTS)
+@pytest.mark.parametrize("tokens", [1, 3, 8, 40])
+def test_activations_beside_an_overflow_keep_their_size(up, tokens):
+    # one h of each token is beyond fp32's range, the others are far beyond fp16's: what the down rows make of them is the
+    # infinity with their weight's sign (binary: no weight is zero), not the difference of two
+    experts, d, f, j = 2, 2048, 128, 5
+    G, D, gw, dw, r = _layer(up, T.Q1_0_G128, d, f, experts, 1.0, 2.0 ** -13)
+    plus = weights(up, 1, d, 0)[0].copy()
+    plus[:] = {T.Q2_0_G128: 0x55, T.T3_5PB_G128: 242, T.Q1_0_G128: 0xFF}[up]  # every t = +1
+    for row in (j, f + j, 2 * f + j, 3 * f + j):
+        G.codes[row] = _dev(plus)[0]
+        G.scales[row] = 65504.0
+    x = np.minimum(np.abs(half(4, tokens, d)).astype(np.float64) * 1e4 + 55e3, 65504).astype(np.float16)
+    # (65504 55e3 2048)^3 = 4.0e38, fp32 ends at 3.4e38; elsewhere at most (6.6e4 2048)^3 = 2.4e24
+    y, _, ids = T.moe(G, D, _dev(r), _dev(x), 1, act="relu2", return_routing=True)
+    want = np.sign(dw[ids.cpu().numpy()[:, 0], :, j]) * np.inf
+    assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
