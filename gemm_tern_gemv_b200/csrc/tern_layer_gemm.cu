@@ -47,7 +47,8 @@ constexpr int kEpiBarrier = 1, kSetBarrier = 2;  // named barriers: the epilogue
 constexpr int epi_warps(bool trans) { return trans ? 4 : 8; }
 constexpr int decoder_sets(bool trans) { return (kThreads / 32 - 4 - epi_warps(trans)) / 4; }
 constexpr uint32_t kTmemCols = 512;  // accumulators at 0 and bn, the A ring from 2 bn on
-constexpr uint64_t kWaitNs = 1000000000ull;
+// Limit of a wait. The epilogue's wait covers a whole sum: that much more for each 64 terms of it (they take about 0.3 us).
+constexpr uint64_t kWaitNs = 1000000000ull, kBlockNs = 1000;
 
 constexpr int X_BYTES = kMaxBN / 2 * BK * 2;  // a CTA's half of the tile's rows of x
 constexpr int P_BYTES = BM * 32;  // codes of a stage: forward 128 rows x 16 or 32 bytes, transposed 64 x 16, 32 or 48
@@ -187,8 +188,8 @@ __device__ __forceinline__ bool bar_all(int id, int threads, bool fine) {
 }
 
 // ---- decoding ------------------------------------------------------------------------------------------
-// Scales from 2^15 on (kBigScale, as fp16 bits): 2 s does not fit fp16. The outputs they belong to are
-// computed term by term in the epilogue instead.
+// Scales from 2^15 on (kBigScale, as fp16 bits): 2 s does not fit fp16. The epilogue leaves out the outputs they
+// belong to; finish_big computes them term by term instead.
 constexpr uint32_t kBigScale = 0x7800;
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
@@ -255,19 +256,6 @@ __device__ __forceinline__ void t3_words(int v5, const uint8_t* p, const uint32_
   }
 }
 
-// A sum whose weights' scales 2 s t cannot hold, term by term: row t of x and output (packed row, transposed:
-// column) `o`, in the accumulators' unit.
-template <int LAYOUT, bool TRANS>
-__device__ __noinline__ float term_by_term(const uint16_t* x, const uint8_t* codes, int64_t cstride, const uint16_t* scales,
-                                           int64_t sstride, int terms, int64_t o) {
-  float z = 0.f;
-  for (int64_t q = 0; q < terms; q++) {
-    const int64_t n = TRANS ? q : o, k = TRANS ? o : q;
-    z = fmaf(h2f(scales[n * sstride + k / kGroup]) * decode_t(LAYOUT, codes + n * cstride, k), h2f(x[q]), z);
-  }
-  return 2.f * z;
-}
-
 // ---- epilogue --------------------------------------------------------------------------------------------
 // 16 rows of x from t0 on of output j: this lane writes the first `lim`. r arrives from tensor memory.
 template <int ACT>
@@ -322,10 +310,81 @@ __device__ __forceinline__ void finish_gated(const Params& p, uint32_t (&r)[16],
   }
 }
 
+template <int LAYOUT, bool TRANS>
+__device__ __forceinline__ void write_outputs(const Params& p, uint32_t (&r)[16], float bias, int64_t t0, int64_t j, int lim, bool up) {
+  constexpr float half = LAYOUT == TERN_Q1_0_G128 ? 1.f : 0.5f;  // the accumulators hold 2 s t x (binary: s t x)
+  if constexpr (TRANS) {
+    uint16_t* y = p.y + t0 * p.nout + j;
+#pragma unroll
+    for (int i = 0; i < 16; i++, y += p.nout)
+      if (i < lim) *y = f2h(__uint_as_float(r[i]) * half);
+  } else {
+    with_act(p.e.act, [&](auto act) {
+      if (p.e.gated) finish_gated<act.value>(p, r, half, bias, t0, j, lim, up);
+      else finish<act.value>(p, r, half, bias, t0, j, lim);
+    });
+  }
+}
+// Row of A, as an output of the tile (gated: of the gate or the up half), that `lane` of the warps at `quad` holds.
+template <int LAYOUT, bool TRANS>
+__device__ __forceinline__ int output_of(int quad, int lane, bool gated) {
+  if (!TRANS) return gated ? quad * 16 + (lane & 15) : quad * 32 + lane;
+  if (LAYOUT == TERN_Q1_0_G128) return 16 * (lane & 7) + 4 * quad + (lane >> 3);
+  return 64 * (quad >> 1) + 8 * (lane & 7) + 4 * (quad & 1) + (lane >> 3);
+}
+
+// The outputs that the epilogue left out, in all tiles of this CTA. Runs when the pipeline is done and tensor memory is
+// free: it may take longer than any wait allows, and nothing waits for it. A warp takes 32 outputs by 16 rows of x.
+template <int LAYOUT, bool TRANS>
+__device__ __noinline__ void finish_big(const Params& p, int rank, int slice, int pair, int pairs, int tiles) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const bool gated = !TRANS && p.e.gated, up = gated && lane >= 16;
+  const auto is_big = [](uint16_t s) { return (s & 0x7fffu) >= kBigScale; };
+  for (int tile = pair; tile < tiles; tile += pairs) {
+    const int64_t r0 = (int64_t)(tile / p.mtiles * 2 + rank) * (gated ? 64 : BM), m0 = (int64_t)(tile % p.mtiles) * p.bn;
+    const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);
+    for (int item = warp; 16 * (item >> 2) < cols; item += kThreads / 32) {
+      const int quad = item & 3, c0 = 16 * (item >> 2);
+      if ((item >> 2) % p.splits != slice) continue;
+      const int64_t j = r0 + output_of<LAYOUT, TRANS>(quad, lane, gated), row = j + (up ? p.nout : 0), t0 = m0 + c0;
+      const bool in = j < p.nout;
+      bool hit = false;
+      if (TRANS) {
+        if (r0 < p.nout)
+          for (int64_t n = lane; n < p.n && !hit; n += 32) hit = is_big(p.scales[n * p.sstride + r0 / kGroup]);
+        hit = __any_sync(0xffffffffu, hit);
+      } else {
+        for (int64_t g = 0; in && !hit && g < p.k / kGroup; g++) hit = is_big(p.scales[row * p.sstride + g]);
+        if (gated) hit |= __shfl_xor_sync(0xffffffffu, hit, 16);
+      }
+      const int lim = in && hit ? cols - c0 : 0;
+      if (!__any_sync(0xffffffffu, lim > 0)) continue;
+      float z[16] = {};
+      if (lim > 0) {
+#pragma unroll 1
+        for (int64_t q = 0; q < p.terms; q++) {
+          const int64_t n = TRANS ? q : row, k = TRANS ? j : q;
+          const float w = h2f(p.scales[n * p.sstride + k / kGroup]) * decode_t(LAYOUT, p.codes + n * p.cstride, k);
+          const uint16_t* x = p.x + t0 * p.xstride + q;
+#pragma unroll
+          for (int i = 0; i < 16; i++, x += p.xstride)
+            if (i < lim) z[i] = fmaf(w, h2f(*x), z[i]);
+        }
+      }
+      __syncwarp();
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 16; i++) r[i] = __float_as_uint(2.f * z[i]);  // the accumulators' unit
+      write_outputs<LAYOUT, TRANS>(p, r, !TRANS && p.e.bias && in ? h2f(p.e.bias[row]) : 0.f, t0, j, lim, up);
+    }
+  }
+}
+
 // ---- the kernel ------------------------------------------------------------------------------------------
 template <int LAYOUT, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1)
-layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
+layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
+                  const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kEpi = epi_warps(TRANS), SETS = decoder_sets(TRANS), kFirstDecoder = 4 + kEpi;
@@ -339,6 +398,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + OFF_MISC + 4);
   uint32_t* lut = reinterpret_cast<uint32_t*>(smem + OFF_LUT);
+  volatile int* left_out = reinterpret_cast<volatile int*>(smem + OFF_MISC + 8);  // the epilogue left outputs to finish_big
   // per tile (in turn) and row of A: a scale of kBigScale or more was met (transposed: row 0 for the whole tile)
   volatile uint8_t* big = smem + OFF_BIG;
 
@@ -361,6 +421,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     for (int i = 0; i < 2; i++) { mbar_init(tfull + i, 1); mbar_init(tempty + i, 2 * kEpi); }
     mbar_init(drain, 1);
     *abort_flag = 0;
+    *left_out = 0;
     fence_mbar_init();
   }
   for (int i = threadIdx.x; i < kBigTiles * BM; i += kThreads) big[i] = 0;
@@ -480,13 +541,9 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
   } else if (warp >= 4 && warp < kFirstDecoder) {
     // ------------------------------------------------------------------ epilogue
     const int quad = warp & 3;
-    // the A row of this lane is output `o` of the tile (of the gate, or with `up` of the up projection)
-    int o;
     const bool up = gated && lane >= 16;
-    if (!TRANS) o = gated ? quad * 16 + (lane & 15) : quad * 32 + lane;
-    else if (LAYOUT == TERN_Q1_0_G128) o = 16 * (lane & 7) + 4 * quad + (lane >> 3);
-    else o = 64 * (quad >> 1) + 8 * (lane & 7) + 4 * (quad & 1) + (lane >> 3);
-    constexpr float half = LAYOUT == TERN_Q1_0_G128 ? 1.f : 0.5f;  // the accumulators hold 2 s t x (binary: s t x)
+    const int o = output_of<LAYOUT, TRANS>(quad, lane, gated);
+    const uint64_t sum_ns = kWaitNs + (uint64_t)kblocks * kBlockNs;
     uint32_t lt = 0;
     for (int tile = pair; tile < tiles; tile += pairs, lt++) {
       const int64_t j = (int64_t)(tile / p.mtiles * 2 + rank) * step + o;  // output column
@@ -495,7 +552,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       const float bias = !TRANS && p.e.bias && in ? h2f(p.e.bias[j + (up ? p.nout : 0)]) : 0.f;
       const uint32_t acc = lt & 1u;
       // the warps leave together, and have all read the tile's flags before any of them is cleared
-      const bool fine = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, kWaitNs);
+      const bool fine = mbar_wait_bounded(tfull + acc, (lt >> 1) & 1u, abort_flag, p.status, TERN_DEVICE_TIMEOUT, sum_ns);
       volatile uint8_t* flag = big + (lt % kBigTiles) * BM + (TRANS ? 0 : quad * 32 + lane);
       const uint32_t taddr = tmem + acc * p.bn + ((uint32_t)(quad * 32) << 16);
       const int cols = (int)(p.m - m0 < p.bn ? p.m - m0 : p.bn);  // rows of x in this tile
@@ -529,12 +586,14 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
       }
       if (!go) break;
       if (again && p.splits == 1) *flag = 0;
+      if (again) *left_out = 1;
+      if (LAYOUT != TERN_Q1_0_G128 && gated) again |= __shfl_xor_sync(0xffffffffu, again, 16);
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = 16 * (slice + p.splits * ((warp >> 2) - 1)); c0 < cols; c0 += 4 * kEpi * p.splits) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(taddr + c0, r);
-        const int lim = in ? cols - c0 : 0;  // rows of x that this lane writes
+        const int lim = in && !again ? cols - c0 : 0;  // rows of x that this lane writes
         const int64_t t0 = m0 + c0;
         tmem_ld_wait();
         for (int i = 1; i < p.splits; i++) {
@@ -542,24 +601,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
 #pragma unroll
           for (int q = 0; q < 16; q++) r[q] = __float_as_uint(__uint_as_float(r[q]) + in[q * BM]);
         }
-        if (again) {
-#pragma unroll
-          for (int i = 0; i < 16; i++)
-            if (i < lim)
-              r[i] = __float_as_uint(term_by_term<LAYOUT, TRANS>(p.x + (t0 + i) * p.xstride, p.codes, p.cstride, p.scales, p.sstride,
-                                                                 p.terms, j + (up ? p.nout : 0)));
-        }
-        if constexpr (TRANS) {
-          uint16_t* y = p.y + t0 * p.nout + j;
-#pragma unroll
-          for (int i = 0; i < 16; i++, y += p.nout)
-            if (i < lim) *y = f2h(__uint_as_float(r[i]) * half);
-        } else {
-          with_act(p.e.act, [&](auto act) {
-            if (gated) finish_gated<act.value>(p, r, half, bias, t0, j, lim, up);
-            else finish<act.value>(p, r, half, bias, t0, j, lim);
-          });
-        }
+        write_outputs<LAYOUT, TRANS>(p, r, bias, t0, j, lim, up);
       }
       tc_fence_before();
       __syncwarp();
@@ -710,6 +752,7 @@ layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_const
     tc_fence_after();
     tmem_dealloc_pair(tmem, kTmemCols);
   }
+  if (LAYOUT != TERN_Q1_0_G128 && *left_out && !*abort_flag) finish_big<LAYOUT, TRANS>(p, rank, slice, pair, pairs, tiles);
 }
 
 cudaLaunchConfig_t config(int clusters, int splits, cudaStream_t st, cudaLaunchAttribute* attr) {
