@@ -82,18 +82,19 @@ cudaError_t launch_rows(RowsParams& p, cudaStream_t st) {
 }
 
 // Int8 digits for one row of x, fp16 column tiles of 8 rows (4 with two slots per unit) for more. The digits take
-// longer to build than a row's fp16 operands, for few tiles longer than they save: us with int8 and with fp16
-//   one row, n x k:    24576 x 4096   4096 x 12288   1000 x 2176   512 x 17408
-//     Q2                12.9 / 13.8    12.2 / 13.1     4.1 / 3.9    13.7 / 12.2
-//     base-3            16.3 / 18.5    16.8 / 17.2     4.2 / 4.2    14.8 / 14.1
-//     binary            10.2 / 15.7     9.9 / 13.4     4.0 / 4.6     9.6 / 10.6
-//   two rows, Q2        14.4 / 13.9    16.9 / 13.5     4.9 / 3.9    19.7 / 13.0
-//     base-3            21.7 / 18.8    24.3 / 17.5     5.6 / 4.3    26.2 / 14.4
-//     binary            13.2 / 16.0    15.0 / 13.9     5.2 / 4.9    16.3 / 11.4
+// longer to build than a row's fp16 operands, for few tiles longer than they save; us with int8 and with fp16:
+//   one row, n x k:    24576 x 4096   12288 x 4096   4096 x 12288   1000 x 2176   512 x 17408
+//     Q2                13.2 / 13.9     9.5 / 9.9     12.3 / 13.1     4.3 / 3.9    13.2 / 11.1
+//     base-3            17.2 / 18.6    12.1 / 12.6    17.9 / 17.1     4.6 / 4.2    15.9 / 14.1
+//     binary            10.2 / 15.6     7.5 / 10.6     9.9 / 13.4     4.1 / 4.7     9.6 / 10.6
+//   two rows, Q2        14.7 / 14.2    11.2 / 10.2    17.2 / 13.5     5.0 / 4.0    18.6 / 11.3
+//     base-3            23.1 / 18.8    16.4 / 12.8    26.7 / 17.4     6.1 / 4.3    28.7 / 14.3
+//     binary            13.2 / 15.9     9.8 / 10.9    15.3 / 14.0     5.3 / 4.9    16.5 / 11.4
 template <int L>
 cudaError_t pick_rows(RowsParams& p, cudaStream_t st) {
   const int64_t tiles = (p.n + 15) / 16, sms = sm_count();  // 16 packed rows to a tile, gated or not
-  if (p.tokens == 1 && (L == TERN_Q1_0_G128 || tiles > sms)) return launch_rows<L, rows::Product<L, rows::kInt8, 1>>(p, st);
+  if (p.tokens == 1 && tiles > (L == TERN_Q1_0_G128 ? 0 : L == TERN_Q2_0_G128 ? sms : 4 * sms))
+    return launch_rows<L, rows::Product<L, rows::kInt8, 1>>(p, st);
   if constexpr (L == TERN_Q1_0_G128)
     if (p.tokens == 2 && tiles > 4 * sms) return launch_rows<L, rows::Product<L, rows::kInt8, 2>>(p, st);
   const int nt = (p.tokens + rows::Geo<L, rows::kFp16>::kTok - 1) / rows::Geo<L, rows::kFp16>::kTok;

@@ -417,9 +417,11 @@ cudaError_t launch_form(const tern_matrix& W, const MoeParams& p, cudaStream_t s
 // f(form) with the form of the product that a call takes: int8 digits for few pairs per expert (on average), else
 // fp16 column tiles. The int8 form decodes faster, but an expert of more than P::kRows pairs (Q2 two, else one) takes
 // it again for the next; 64 experts of 2048 x 1024, 8 chosen, us with int8 and with fp16:
-//   pairs per expert   1/2        1          2                    1/2        1          2                 1          2
-//   Q2                 43 / 46    53 / 57    68 / 66    base-3    53 / 57    71 / 73    109 / 87    binary  52 / 70    71 / 83
-// (base-3 with 128 experts of 2048 x 768 and one pair: 95 / 92). Two column tiles where an expert's pairs often need
+//   pairs per expert   1/2        3/4        1          2
+//   Q2                 45 / 47    49 / 52    55 / 57    70 / 67
+//   base-3             56 / 58    66 / 67    76 / 73   116 / 87     (128 experts of 2048 x 768: 70 / 73, 86 / 84, 101 / 93)
+//   binary             42 / 57    48 / 62    52 / 69    72 / 82
+// Two column tiles where an expert's pairs often need
 // them; eight experts of 4096 x 12288, 2 chosen, us with one and with two:
 //   pairs per expert   4            8            16
 //   Q2                 153 / 206    193 / 218    302 / 297
@@ -429,7 +431,7 @@ template <class P> struct Form { using type = P; };
 template <int L, class F>
 auto with_form(int tokens, int top_k, int experts, F f) {
   const int pairs = tokens * top_k;
-  const int few = L == TERN_Q1_0_G128 ? 2 * experts : L == TERN_Q2_0_G128 ? experts : experts - 1;
+  const int few = L == TERN_Q1_0_G128 ? 2 * experts : L == TERN_Q2_0_G128 ? experts : experts / 2;
   if (tokens == 1 || pairs <= few) return f(Form<rows::Product<L, rows::kInt8, 1>>{});
   if (pairs < (L == TERN_Q2_0_G128 ? 14 : 4) * experts) return f(Form<rows::Product<L, rows::kFp16, 1>>{});
   return f(Form<rows::Product<L, rows::kFp16, 2>>{});

@@ -17,7 +17,11 @@
 //       binary  word & (0x01.. << j) is 2^j b (t = 2 b - 1), B holds X / 2^j, start -sum X / 2.
 //       base-3  quotients q_j = floor(v / 3^j): c_j = q_j - 3 q_{j+1}, so B holds X_j - 3 X_{j-1} and the
 //               accumulators start at -sum X; q_{j+1} = (85 q_j + 80) >> 8 for every q_j <= 242.
-//     All of that is exact in int32; an activation is off by at most 2^-27 of the largest of its slot.
+//     All of that is exact in int32; an activation is off by at most 2^-27 of the largest of its slot. For binary, whose
+//     weights are never zero, that is less than the error of the sum in fp32. Where they can be zero an output may depend on
+//     the small activations alone, so what the rounding takes from the caller's is added in fp32 afterwards (add_lost;
+//     of fp16 activations it takes nothing unless a slot holds one of 16 or more beside one 2^17 times smaller). The
+//     experts' own h keep the rounding.
 //   fp16 (up to 8 rows per tile; 4 with two slots): x itself is the B operand, the codes become +-2 / 0 by
 //     one multiply and one mask per two weights, fp32 accumulators restart at every unit.
 // Either way each unit's sums take their group scale in fp32. The activation operands of a CTA are built
@@ -125,6 +129,7 @@ __device__ __forceinline__ int exponent(uint32_t abs_bits) { return (int)(abs_bi
 // consecutive activations as floats, load16() N (a multiple of 8) as fp16 bits; both are zero from K on.
 // K is a multiple of 8 and so are load16's k0 and, unless NE is 5, load's k0 of NE; rows are 16-byte aligned.
 struct HalfRows {
+  static constexpr bool kExact = true;  // the int8 form has to make its rounding good
   const uint16_t* base;
   int64_t stride;
   const int* index;  // row t of the product is row index[t] of base (null: t)
@@ -155,6 +160,7 @@ struct HalfRows {
   }
 };
 struct FloatRows {
+  static constexpr bool kExact = false;
   const float* base;
   int64_t stride;
   const int* index;
@@ -189,19 +195,17 @@ struct FloatRows {
 };
 
 // ---- building the activation operands -----------------------------------------------------------------
-// int8 form of one unit u of one row of x, the tok-th of its column tile. xv: this lane's activations. scr: 32 x 8 words of this warp;
-// frag: the column tile's entries, then one 16-byte record for each q: accumulator starts of columns 2 q
-// and 2 q + 1 (binary: their sum to be added to twice the accumulators) and the scale 2^-S (x 2^16 for
-// digits 2 and 3). Non-finite activations count as zero here (the caller adds them apart) and set *odd.
+// First weight of unit u that belongs to slot 1.
 template <int L>
-__device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int tok, int u, uint32_t* scr, uint4* frag, int* odd) {
-  using T = Lay<L>;
-  using G = Geo<L, kInt8>;
+__device__ __forceinline__ int slot_edge(int u) {
+  return Lay<L>::kSlots == 1 ? Lay<L>::kUnitK : (L == TERN_Q1_0_G128 ? 128 : 128 - (u * 160) % 128);
+}
+// Exponents S of the slots of a unit, from the largest finite |x|: the integers are round(x 2^(S - sh)), sh by code_shift.
+// xv: this lane's activations, those of the weights of byte `lane`; non-finite ones become zero (true if there was one).
+template <int L>
+__device__ __forceinline__ bool slot_exponents(float (&xv)[Lay<L>::kUnitK / 32], int edge, int (&S)[2]) {
+  constexpr int NE = Lay<L>::kUnitK / 32;
   const int lane = threadIdx.x & 31;
-  constexpr int NE = T::kUnitK / 32;  // activations of this lane: the weights of byte `lane` of the unit
-  constexpr bool two_in_a_byte = L == TERN_T3_5PB_G128;  // a byte may hold weights of both slots
-  // first weight of the unit that belongs to slot 1
-  const int edge = T::kSlots == 1 ? T::kUnitK : (L == TERN_Q1_0_G128 ? 128 : 128 - (u * 160) % 128);
   uint32_t mx[2] = {0, 0};
   bool bad = false;
 #pragma unroll
@@ -216,14 +220,38 @@ __device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int
     mx[0] = max(mx[0], s ? 0u : b);
     mx[1] = max(mx[1], s ? b : 0u);
   }
-  if (__any_sync(0xffffffffu, bad) && lane == 0) *odd = 1;
   constexpr int kTop = L == TERN_T3_5PB_G128 ? 28 : 30;  // base-3 operands add up to four activations
-  int S[2] = {0, 0};
+  S[0] = S[1] = 0;
 #pragma unroll
-  for (int s = 0; s < T::kSlots; s++) {
+  for (int s = 0; s < Lay<L>::kSlots; s++) {
     mx[s] = __reduce_max_sync(0xffffffffu, mx[s]);
     S[s] = mx[s] ? min(100, kTop - exponent(mx[s])) : 0;
   }
+  return bad;
+}
+// The code operand of weight e of a byte is 2^sh times c (or b).
+template <int L> __device__ __forceinline__ constexpr int code_shift(int e) {
+  return L == TERN_Q2_0_G128 ? 2 * (e & 1) : L == TERN_Q1_0_G128 ? (e & 3) : 0;
+}
+
+// int8 form of one unit u of one row of x, the tok-th of its column tile. xv: this lane's activations. scr: 32 x 8 words of this warp;
+// frag: the column tile's entries, then one 16-byte record for each q: accumulator starts of columns 2 q
+// and 2 q + 1 (binary: their sum to be added to twice the accumulators) and the scale 2^-S (x 2^16 for
+// digits 2 and 3). Non-finite activations count as zero here (the caller adds them apart) and set *odd. lost (EXACT): bit
+// u mod 1024 is set if an activation was rounded.
+template <int L, bool EXACT>
+__device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int tok, int u, uint32_t* scr, uint4* frag, int* odd, uint32_t* lost) {
+  using T = Lay<L>;
+  using G = Geo<L, kInt8>;
+  const int lane = threadIdx.x & 31;
+  constexpr int NE = T::kUnitK / 32;  // activations of this lane: the weights of byte `lane` of the unit
+  constexpr bool two_in_a_byte = L == TERN_T3_5PB_G128;  // a byte may hold weights of both slots
+  const int edge = slot_edge<L>(u);
+  int S[2];
+  if (__any_sync(0xffffffffu, slot_exponents<L>(xv, edge, S)) && lane == 0) *odd = 1;
+  // every fp16 activation is a multiple of 2^-24
+  const bool coarse = EXACT && min(S[0], T::kSlots == 2 ? S[1] : S[0]) < 24 + code_shift<L>(1);
+  bool rounded = false;
   const int w = lane >> 2, pl = lane & 3;  // the word and the digit that this lane gathers
   const uint32_t sel = (uint32_t)pl | ((uint32_t)(pl + 4) << 4);
   auto plane = [&](const uint32_t* d4) {  // digit pl of four consecutive scratch words
@@ -237,7 +265,9 @@ __device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int
       int xi[5], sum = 0;
 #pragma unroll
       for (int e = 0; e < 5; e++) {
-        xi[e] = ((lane * 5 + e < edge) == (s == 0)) ? __float2int_rn(xv[e] * exp2i(Ss)) : 0;
+        const float v = ((lane * 5 + e < edge) == (s == 0)) ? xv[e] * exp2i(Ss) : 0.f;
+        xi[e] = __float2int_rn(v);
+        if (coarse) rounded |= rintf(v) != v;
         sum += xi[e];
       }
 #pragma unroll
@@ -246,8 +276,9 @@ __device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int
     } else {
 #pragma unroll
       for (int e = 0; e < NE; e++) {
-        const int sh = L == TERN_Q2_0_G128 ? 2 * (e & 1) : (e & 3);  // the code operand is 2^sh times c (or b)
-        scr[e * 32 + lane] = digits(__float2int_rn(xv[e] * exp2i(Ss - sh)));
+        const float v = xv[e] * exp2i(Ss - code_shift<L>(e));
+        if (coarse) rounded |= rintf(v) != v;
+        scr[e * 32 + lane] = digits(__float2int_rn(v));
       }
     }
     __syncwarp();
@@ -275,6 +306,7 @@ __device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int
                      __float_as_uint(exp2i((pl ? 16 : 0) - Ss)), 0u);
     __syncwarp();
   }
+  if (coarse && __any_sync(0xffffffffu, rounded) && lane == 0) atomicOr(lost + (u >> 5 & 31), 1u << (u & 31));
 }
 
 // fp16 form of one (unit, column tile from row t0 of x on): lane (g, q) loads and writes the operand words of
@@ -398,13 +430,14 @@ struct Product {
   // 4-byte boundary below the first on
   static constexpr int kScaleBytes = L == TERN_Q2_0_G128 ? 8 : 16;
   static constexpr int kStage = 16 * 128 + 16 * kScaleBytes;  // [16][128] codes, [16][kScaleBytes] scales
+  static constexpr int kFlags = 64 + (MODE == kInt8 ? 128 : 0);  // bytes: `odd`, `lost`
   static bool plan(int tiles, int units, size_t room, Split* out);
 
   // shared memory: operands [pass], partial sums [batch][wk][16][kRows], flags, scratch of the int8 operands'
   // building, rings
   static __host__ __device__ size_t part_bytes(const Split& s) { return (size_t)s.batch * s.wk * 16 * kRows * 4; }
   static __host__ __device__ size_t smem_bytes(const Split& s) {
-    return (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s) + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + kMaxWarps * kDepth * kStage + 64 + 128;
+    return (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s) + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + kMaxWarps * kDepth * kStage + kFlags + 128;
   }
 
   // copy cursor: this lane's four rows (lane / 8 + 4 i) of the tile's codes at its 16-byte piece of the block,
@@ -413,6 +446,7 @@ struct Product {
   const uint16_t* ps;
   int lt, lb;
   uint32_t kx, ky;  // see operands8
+  int carry;        // base-3, int8: all ones above bit 16 in lanes of the low digits
 
   __device__ __forceinline__ void set_rows(const Mat& M, const Map& R) {
     const int lane = threadIdx.x & 31;
@@ -478,6 +512,13 @@ struct Product {
         if (L == TERN_Q1_0_G128) {  // t = 2 b - 1
           v0 = 2 * v0 + (int)st[n].x;
           v1 = 2 * v1 + (int)st[n].x;
+        }
+        if (L == TERN_T3_5PB_G128) {
+          // The digits of X_j - 3 X_{j-1} carry: what weights of zero leave is zero only in both lanes of a sum together, and
+          // 2^16 more in one of them than the sum may be. So the carry goes over.
+          const int o0 = (v0 + 0x8000) & carry, o1 = (v1 + 0x8000) & carry;
+          v0 += (__shfl_xor_sync(0xffffffffu, o0, 1) >> 16) - o0;
+          v1 += (__shfl_xor_sync(0xffffffffu, o1, 1) >> 16) - o1;
         }
         const float sc = __uint_as_float(st[n].z);
         acc[n][0] = fmaf(s0 * sc, (float)v0, acc[n][0]);
@@ -555,6 +596,65 @@ struct Product {
     }
   }
 
+  // Adds what the integers leave out of the activations in the units marked in `lost` to the first partial sums of tiles
+  // [b0, b1): a warp takes four rows of a tile, a lane its byte of each unit. Units of an equal mark add zeros.
+  template <class X>
+  static __device__ __forceinline__ void add_lost(const uint32_t* lost, float* part, int wk, const Mat& M, const Map& R, int b0, int b1,
+                                               const X& xs, int tokens) {
+    constexpr int NE = T::kUnitK / 32;
+    const int lane = threadIdx.x & 31;
+    const uint32_t marks = lost[lane];
+    for (int item = threadIdx.x >> 5; item < (b1 - b0) * 4; item += kMaxWarps) {
+      const int tl = item >> 2, r0 = 4 * (item & 3);
+      const int64_t o = (int64_t)(b0 + tl) * R.step, last = min((int64_t)R.limit - 1 - o, (int64_t)64);
+      const int64_t base = (r0 < 8 ? R.first : R.second) + o;
+      const int at = r0 < 8 ? r0 : r0 - 8 + R.ahead;
+      for (int c = 0; c < M.units; c += 1024)
+        for (int w = 0; w < 32; w++)
+          for (uint32_t bits = __shfl_sync(0xffffffffu, marks, w); bits; bits &= bits - 1) {
+            const int u = c + 32 * w + __ffs(bits) - 1;
+            if (u >= M.units) break;
+            const int edge = slot_edge<L>(u), byte = 32 * u + lane, g = u * T::kUnitK / kGroup;
+            for (int t = 0; t < tokens; t++) {
+              float xv[NE] = {};
+              xs.template load<NE>(t, u * T::kUnitK + lane * NE, M.K, xv);
+              int S[2];
+              slot_exponents<L>(xv, edge, S);
+#pragma unroll
+              for (int e = 0; e < NE; e++) {
+                const int Ss = S[lane * NE + e < edge ? 0 : 1] - code_shift<L>(e);
+                const float v = xv[e] * exp2i(Ss);
+                xv[e] = (v - rintf(v)) * exp2i(-Ss);
+              }
+#pragma unroll
+              for (int i = 0; i < 4; i++) {
+                const int64_t row = base + min((int64_t)(at + i), last);
+                const uint16_t* s = M.scales + row * M.sstride;
+                const float s0 = h2f(s[g]), s1 = h2f(s[min(g + 1, M.groups - 1)]);
+                int code = byte < M.row_bytes ? M.codes[row * M.cstride + byte] : 0;
+                float z = 0.f;
+#pragma unroll
+                for (int e = 0; e < NE; e++) {
+                  int c3 = (code & 1) - (code & 2);
+                  if constexpr (L == TERN_T3_5PB_G128) {
+                    const int q = code / 3;
+                    c3 = code - 3 * q - 1;
+                    code = q;
+                  } else {
+                    code >>= 2;
+                  }
+                  // (a scale that is not finite does not meet activations that are whole)
+                  if (xv[e] != 0.f) z = fmaf((lane * NE + e < edge ? s0 : s1) * (float)c3, xv[e], z);
+                }
+#pragma unroll
+                for (int d = 16; d; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+                if (lane == 0) part[(size_t)tl * wk * 16 * kRows + (r0 + i) * kRows + t] += z;
+              }
+            }
+          }
+    }
+  }
+
   // Tiles [t0, t1) of M's rows by R times rows [0, tokens) of xs. For every output row and row of x
   // fin(tile, r, t, z, -) gets the sum of tile row r, or with R.ahead == 0 (gate and up rows)
   // fin(tile, r, t, z_gate, z_up) for r < 8. All threads of the CTA call this together; `first` is called
@@ -568,14 +668,16 @@ struct Product {
     float* part = reinterpret_cast<float*>(smem + (size_t)s.pass * kBlk * kUnitBytes);
     uint8_t* tail = smem + (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s);
     int* odd = reinterpret_cast<int*>(tail);  // rows of x with a non-finite activation
-    uint32_t* scr = reinterpret_cast<uint32_t*>(tail + 64) + warp * 256;
-    const uint32_t ring = ((sm100::smem_u32(tail) + 64 + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 127) & ~127u) + warp * (kDepth * kStage);
+    uint32_t* lost = reinterpret_cast<uint32_t*>(tail + 64);  // int8: bit u mod 1024: activations of unit u were rounded
+    uint32_t* scr = reinterpret_cast<uint32_t*>(tail + kFlags) + warp * 256;
+    const uint32_t ring = ((sm100::smem_u32(tail) + kFlags + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 127) & ~127u) + warp * (kDepth * kStage);
     const int blocks = (M.units + kBlk - 1) / kBlk;
     const int wk = min(s.wk, blocks);  // (M may be shorter than what was planned for)
     const float inv_wk = __fdividef(1.f, (float)wk), inv_tg = __fdividef(1.f, (float)s.tg);
     const int tg = part_of(warp, inv_wk), kg = warp - tg * wk;
     kx = L == TERN_Q2_0_G128 ? 0xAAAAAAAAu : 85u;
     ky = 0x00500050u;
+    carry = q & 1 ? 0 : ~0xffff;
     asm volatile("" : "+r"(kx), "+r"(ky));
     // This lane's entry of a column tile's operands: column g, k by q. Columns of absent rows of x read
     // those of a present one (their sums are never looked at).
@@ -600,7 +702,9 @@ struct Product {
     const int whole = R.limit / R.step;  // tiles that are not cut short
     const uint32_t lane_c = (uint32_t)(g * 128 + (g & 3) * 32 + 8 * q);  // unit 0 of row g in a stage
     bool fresh = true;
+    constexpr bool kLost = MODE == kInt8 && L != TERN_Q1_0_G128 && X::kExact;
     if (tid < 16) odd[tid] = 0;
+    if (kLost && tid < 32) lost[tid] = 0;
     for (int b0 = t0; b0 < t1; b0 += s.batch) {
       const int b1 = min(t1, b0 + s.batch);
       int ta = b0, tb = b0;
@@ -659,8 +763,8 @@ struct Product {
               for (int e = 0; e < NE; e++) xv[e] = ahead[e];
               fetch(i + kMaxWarps);
               const int t = kRows == 1 || i < nu ? 0 : 1, u = i < nu ? i : i - nu;
-              build_int8<L>(xv, t % G::kTok, u0 + u, scr, reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes),
-                            odd + t);
+              build_int8<L, kLost>(xv, t % G::kTok, u0 + u, scr, reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes),
+                            odd + t, lost);
             }
           } else {
             uint32_t ahead[kLaneWords<L>] = {};
@@ -739,6 +843,12 @@ struct Product {
         copy_wait<0>();
       }
       __syncthreads();
+      if constexpr (kLost) {
+        if (__any_sync(0xffffffffu, lost[lane] != 0)) {
+          add_lost(lost, part, wk, M, R, b0, b1, xs, tokens);
+          __syncthreads();
+        }
+      }
       // the wk partial sums of each output, in order
       const bool pairs = R.ahead == 0;
       const int rows = pairs ? 8 : 16, shift = pairs ? 3 : 4;
