@@ -69,8 +69,9 @@ __device__ __forceinline__ void act_both(int act, float z, float* f, float* df) 
   if (act == TERN_ACT_SILU || act == TERN_ACT_GELU_TANH) {
     const float u = act == TERN_ACT_SILU ? z : gelu_tanh_u(z);
     // sigmoid s = 1 / (1 + e^-u) and its complement e^-u s (not 1 - s: the tails keep their relative precision);
-    // past e^80 both products with z vanish in fp32 alike
-    const float e = __expf(fminf(-u, 80.f)), s = __fdividef(1.f, 1.f + e), c = e * s;
+    // Past e^88 the quotient is 0 (its divisor lies between 2^126 and 2^128, where this division gives that): both products
+    // with a finite z vanish, as they do in fp32 anyhow, and -inf gives NaN as in the formulas.
+    const float e = __expf(fminf(-u, 88.f)), s = __fdividef(1.f, 1.f + e), c = e * s;
     const float du = act == TERN_ACT_SILU ? 1.f : 1.5957691216057308f * (1.f + 0.134145f * z * z);
     *f = z * s;
     *df = s + z * s * c * du;
