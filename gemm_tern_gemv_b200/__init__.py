@@ -582,7 +582,8 @@ def moe(gate_up: TernMatrix, down: TernMatrix, router, x, top_k: int, act: str =
         residual=None, y=None, workspace=None, return_routing: bool = False):
     """A whole mixture-of-experts layer for up to MOE_MAX_TOKENS tokens (tern_moe): x fp16 [tokens][d] is routed by
     softmax(x router^T), router fp16 [experts][d], to the top_k most probable experts (ties to the lower index), and
-    y = sum over them of p * down_e(act(gate_e x) * up_e x) (+ residual).
+    y = sum over them of p * down_e(act(gate_e x) * up_e x) (+ residual). All in fp32 but act(gate_e x) * up_e x, which
+    goes to down_e in fp16's 11 bits, or more where few tokens share an expert (tern.h has the figures).
 
     gate_up: packed [experts * 2f][d], for each expert f gate rows and then f up rows; down: packed [experts * d][f].
     workspace: a uint8 tensor of moe_workspace_bytes() (any contents; allocated when None). With return_routing

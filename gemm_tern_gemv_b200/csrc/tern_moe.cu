@@ -13,8 +13,11 @@
 //   up     the (token, expert) pairs are sorted by expert; the 8-output tiles (gate and up rows) of all experts
 //          in use form one list that is dealt evenly to one CTA per SM. The products are those of
 //          tern_rows.cuh. h = act(g) u in fp32.
-//   down   the same over 16-row tiles of the down matrices, with h brought into fp16's range by a power of two
-//          per pair, and over slices of K where f is long. Sums of a pair and slice go to the workspace.
+//   down   the same over 16-row tiles of the down matrices and over slices of K where f is long. Sums of a pair and
+//          slice go to the workspace. What h loses: the int8 form takes it as integers, off by 2^-27 of the largest
+//          of its slot; the fp16 form rounds it to fp16, brought into range by a power of two per pair (2^-11 of
+//          itself). Two fp16 terms for each h would keep 22 bits, for twice the MMAs and operand reads of a kernel
+//          that shared memory already holds up; one is what a layer with fp16 activations between its products has.
 //   combine  adds a token's pairs up, in the order of j and of the slices.
 #include "tern_rows.cuh"
 

@@ -400,8 +400,13 @@ TERN_API size_t tern_moe_workspace_bytes(const tern_moe_layer* layer, int64_t to
  *   p = softmax(router x[t]); ids[t] = the top_k most probable experts, most probable first, ties to
  *   the lower index; weights[t][j] = p[ids[t][j]] (divided by their sum with renormalize);
  *   y[t] = sum_j weights[t][j] * down_e (act(gate_e x[t]) * (up_e x[t])) + residual[t],  e = ids[t][j].
- * Logits and their order in fp64, everything else in fp32, y rounded once. Experts without a token are
- * not read. A token whose logits hold a NaN gets valid ids and NaN weights.
+ * Logits and their order in fp64, products, activations and sums in fp32, y rounded once. Only between
+ * the two products h = act(gate_e x) * (up_e x) is held in fewer bits. With few (token, expert) pairs per
+ * expert it is taken as integers: off by at most 2^-27 of the largest of the 128 to 256 h around it. Else it
+ * is taken as fp16, times a power of two that brings the pair's largest finite h to [2^14, 2^15): off by
+ * at most 2^-11 of itself and 2^-39 of that largest. Which of the two goes by down's layout, tokens, top_k
+ * and experts, so a token's y may differ by such roundings with the number of tokens in the call.
+ * Experts without a token are not read. A token whose logits hold a NaN gets valid ids and NaN weights.
  *   x  device fp16 [tokens][d], 16-byte aligned;  y  device fp16 [tokens][d]
  *   residual   device fp16 [tokens][d] or NULL; may be y or x
  *   weights    device fp32 [tokens][top_k] or NULL;  ids  device int32 [tokens][top_k] or NULL

@@ -61,3 +61,18 @@ def test_activations_beside_an_overflow_keep_their_size(up, tokens):
     y, _, ids = T.moe(G, D, _dev(r), _dev(x), 1, act="relu2", return_routing=True)
     want = np.sign(dw[ids.cpu().numpy()[:, 0], :, j]) * np.inf
     assert np.array_equal(y.cpu().numpy().astype(np.float64), want)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("tokens,experts,top_k,held", [(1, 4, 2, "integers"), (4, 64, 8, "integers"), (3, 24, 4, "integers"),
+                                                      (4, 6, 3, "fp16"), (16, 4, 2, "fp16"), (30, 2, 1, "fp16")])
+def test_activations_are_held_as_documented(layout, tokens, experts, top_k, held):
+    # one token and up to half a pair per expert: integers; from two pairs (binary: more) on: fp16
+    d, f = 256, 640
+    if layout == T.Q1_0_G128 and held == "fp16":
+        tokens *= 2
+    G, D, gw, dw, r = _layer(layout, layout, d, f, experts, 0.02, 0.02, seed=20)
+    x = half(21, tokens, d)
+    args = (gw, dw, f64(r), f64(x), top_k, "silu", True)
+    y = T.moe(G, D, _dev(r), _dev(x), top_k)
+    check(y.cpu().numpy(), L.moe(*args)[0], L.moe_bound(*args, held=held), f"{held} {layout}")
