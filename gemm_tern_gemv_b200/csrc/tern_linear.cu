@@ -103,12 +103,18 @@ cudaError_t pick_rows(RowsParams& p, cudaStream_t st) {
   return launch_rows<L, rows::Product<L, rows::kFp16, 4>>(p, st);
 }
 
-// Rows of x that the register core takes. Above eight rows the operands of base-3 and binary (four column tiles, half
-// of them zeros) stop fitting into shared memory at about k = 5120 and are built again for every few tiles: 16 rows x
-// 4096 x 12288 took 45 us base-3 and 37 binary, against 32 and 26 on the tensor cores of the other kernel; x 4096 x 4096
-// 17.6 and 13.5 against 19.2 and 16.7.
+// Rows of x that the register core takes. Operands of nine rows and more stay in shared memory up to k = 1920 (base-3:
+// four column tiles, half of them zeros), 4096 (binary, the same) and 4608 (Q2, two tiles); longer rows take them in
+// passes, built again for every few tiles of a CTA. us on this core and on the tensor cores of the other kernel:
+//                   4096 x 4096   4096 x 5120   24576 x 5120   4096 x 12288   5120 x 17408
+//   Q2       9 rows    8.5 / 16.8   12.1 / 18.1   28.4 / 47.6    20.1 / 27.2    33.9 / 34.1
+//           16         9.4 / 16.9   13.3 / 18.1   31.0 / 47.8    22.8 / 27.4    38.1 / 34.3
+//   base-3   9        16.7 / 18.6   19.6 / 20.2   48.1 / 57.9    42.1 / 31.5    66.5 / 40.2
+//           16        17.7 / 18.7   20.8 / 20.4   50.9 / 58.0    45.0 / 31.7    70.7 / 40.4
+//   binary   9        11.4 / 15.5   17.7 / 16.9   43.2 / 43.8    31.1 / 25.8    53.9 / 32.1
+//           16        13.2 / 15.7   20.6 / 17.2   47.3 / 43.9    37.3 / 25.9    63.1 / 32.4
 bool few_rows(const tern_matrix& W, int64_t m) {
-  return m <= 8 || (m <= 16 && (W.layout == TERN_Q2_0_G128 || W.k <= 5120));
+  return m <= 8 || (m <= 16 && (W.layout == TERN_Q2_0_G128 || W.k <= (W.layout == TERN_T3_5PB_G128 ? 5120 : 4096)));
 }
 
 }  // namespace

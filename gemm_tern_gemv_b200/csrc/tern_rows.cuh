@@ -28,11 +28,15 @@
 // once in shared memory, in the order the MMA lanes read them.
 //
 // What bounds it: for small matrices the way in (entry and first requests about 2000 cycles, operands 2500 a row of
-// 4096) and out; 4096 x 4096 Q2, one row, 6.0 us. For large ones the issue of instructions: a unit of 16 rows takes a
-// warp 95 (Q2, int8), 129 (Q2, fp16, one column tile) or 159 (base-3, int8) of them; 24576 x 4096 at one row 13.0 us
-// Q2 = 2.1 TB/s, 16.2 base-3, 10.2 binary; 26.8 Q2 at 16 rows. With two column tiles and more the operands' reads
-// from shared memory (512 bytes for two MMAs) come close to that. Why copies run through shared memory: with loads
-// into registers a warp has too few bytes in flight (25 us there), and 128-byte pieces of a row keep DRAM's pages open.
+// 4096) and out; 4096 x 4096 Q2, one row, 6.1 us. For large ones latency, with the four warps a scheduler that the
+// registers leave: at 24576 x 4096 and one row issue slots are 44 % busy with Q2 (49 % base-3), the shared-memory pipe
+// 36 % (34 %), DRAM 21 % (13 %). Of 8.8 warp cycles an instruction 1.9 go to waiting for copies, 1.9 to fixed latencies, 0.9 to
+// shared memory, 0.8 to barriers; base-3 spends 1.9 of 8.0 at barriers, where its 10 or 11 tiles x 7 blocks leave warps
+// idle. A unit of 16 rows takes a warp 95 (Q2, int8), 129 (Q2, fp16, one column tile) or 171 (base-3, int8)
+// instructions; 13.1 us Q2 = 2.1 TB/s, 17.2 base-3, 10.2 binary; 26.9 Q2 at 16 rows. With two column tiles and more the
+// operands' reads from shared memory (512 bytes for two MMAs) come close to its limit. Why copies run through shared
+// memory: with loads into registers a warp has too few bytes in flight (25 us there), and 128-byte pieces of a row keep
+// DRAM's pages open.
 #pragma once
 
 #include "sm100.cuh"
