@@ -96,3 +96,25 @@ def test_experts_of_one_token(layout):
     y, _, ids = T.moe(G, D, _dev(r), _dev(x), 2, act="relu", return_routing=True)
     assert np.array_equal(ids.cpu().numpy(), L.moe(*args)[2])
     check(y.cpu().numpy(), L.moe(*args)[0], L.moe_bound(*args, held="integers"), "one token")
+
+
+@pytest.mark.parametrize("layout", [T.Q2_0_G128, T.T3_5PB_G128])
+def test_experts_that_two_tokens_share(layout):
+    # few pairs per expert, some of them with two: huge activations whose weights are zero beside tiny ones in each
+    experts, d, f, tokens, top_k = 24, 640, 384, 3, 4
+    from tests.gpu_cases import pack_rows
+    _, gs, gw = weights(layout, experts * 2 * f, d, 11)
+    dc, ds, dw = weights(layout, experts * d, f, 12, scale=64.0)
+    x = _outliers(13, tokens, d, 1e-3, 320)
+    big = (np.abs(x) > 1).any(0)
+    t = np.sign(gw).astype(np.int8)
+    t[:, big] = 0
+    gw = np.where(big, 0.0, gw)
+    G = T.from_packed(_dev(pack_rows(t, layout)), _dev(gs), layout, d)
+    D = T.from_packed(_dev(dc), _dev(ds), layout, f)
+    r = half(14, experts, d, scale=1e-3)
+    args = (gw.reshape(experts, 2 * f, d), dw.reshape(experts, d, f), f64(r), f64(x), top_k, "relu", True)
+    y, _, ids = T.moe(G, D, _dev(r), _dev(x), top_k, act="relu", return_routing=True)
+    assert np.array_equal(ids.cpu().numpy(), L.moe(*args)[2])
+    assert np.bincount(ids.cpu().numpy().ravel()).max() > 1
+    check(y.cpu().numpy(), L.moe(*args)[0], L.moe_bound(*args, held="integers"), "shared experts")
