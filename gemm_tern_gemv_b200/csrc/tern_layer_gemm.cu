@@ -336,7 +336,7 @@ __device__ __forceinline__ int output_of(int quad, int lane, bool gated) {
 // The outputs that the epilogue left out, in all tiles of this CTA. Runs when the pipeline is done and tensor memory is
 // free: it may take longer than any wait allows, and nothing waits for it. A warp takes 32 outputs by 16 rows of x.
 template <int LAYOUT, bool TRANS>
-__device__ __noinline__ void finish_big(const Params& p, int rank, int slice, int pair, int pairs, int tiles) {
+__device__ __noinline__ void finish_big(const Params p, int rank, int slice, int pair, int pairs, int tiles) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const bool gated = !TRANS && p.e.gated, up = gated && lane >= 16;
   const auto is_big = [](uint16_t s) { return (s & 0x7fffu) >= kBigScale; };
@@ -383,8 +383,7 @@ __device__ __noinline__ void finish_big(const Params& p, int rank, int slice, in
 // ---- the kernel ------------------------------------------------------------------------------------------
 template <int LAYOUT, bool TRANS>
 __global__ void __launch_bounds__(kThreads, 1)
-layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w,
-                  const __grid_constant__ Params p) {
+layer_gemm_kernel(const __grid_constant__ CUtensorMap tmap_x, const __grid_constant__ CUtensorMap tmap_w, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   constexpr int kEpi = epi_warps(TRANS), SETS = decoder_sets(TRANS), kFirstDecoder = 4 + kEpi;
