@@ -4,9 +4,9 @@
 //
 // The least is to read the packed weights of the experts in use once. What it takes is decoding: a segment of an
 // expert's pairs goes through the expert's weights as one product, so two segments decode them twice. 16 tokens,
-// 128 base-3 experts of 2048 x 768: 92 us (route 11, up 43, down 33, combine 3); 64 tokens, 8 Q2 experts of 4096 x
-// 12288: 297 us (up 170, down 115), of which the tensor cores are busy a third and shared memory two thirds; one
-// token, 8 of 64 Q2 experts of 2048 x 1024: 30 us, about as long as the launches take the host.
+// 128 base-3 experts of 2048 x 768: 94 us (route 11, up 43, down 33, combine 3); 64 tokens, 8 Q2 experts of 4096 x
+// 12288: 298 us (up 170, down 115), where up keeps shared memory 58 % busy, the tensor pipe 38 and issue 49; one
+// token, 8 of 64 Q2 experts of 2048 x 1024: 31 us, about as long as the launches take the host.
 // Four launches, each started while the one before ends (programmatic dependent launch):
 //   route  a cluster of eight CTAs for one to four tokens: each computes the logits of every eighth expert,
 //          the first collects them through the cluster's shared memory and picks.

@@ -19,9 +19,11 @@
 //               accumulators start at -sum X; q_{j+1} = (85 q_j + 80) >> 8 for every q_j <= 242.
 //     All of that is exact in int32; an activation is off by at most 2^-27 of the largest of its slot. For binary, whose
 //     weights are never zero, that is less than the error of the sum in fp32. Where they can be zero an output may depend on
-//     the small activations alone, so what the rounding takes from the caller's is added in fp32 afterwards (add_lost;
-//     of fp16 activations it takes nothing unless a slot holds one of 16 or more beside one 2^17 times smaller). The
-//     experts' own h keep the rounding.
+//     the small activations alone, so what the rounding takes from the caller's is added afterwards (of fp16 activations
+//     it takes nothing unless a slot holds one of 16 or more beside one 2^17 times smaller): up to kMaxLost of them from
+//     a list, more by add_lost. 24576 x 4096 Q2, one row, 12.8 us without
+//     one, 14.7 with one such unit, 16.0 with one of 1500 in every unit beside N(0, 1), 93 where every activation is rounded
+//     (base-3 17.0, 19.3, 20.9, 172). The experts' own h keep the rounding.
 //   fp16 (up to 8 rows per tile; 4 with two slots): x itself is the B operand, the codes become +-2 / 0 by
 //     one multiply and one mask per two weights, fp32 accumulators restart at every unit.
 // Either way each unit's sums take their group scale in fp32. The activation operands of a CTA are built
@@ -238,13 +240,23 @@ template <int L> __device__ __forceinline__ constexpr int code_shift(int e) {
   return L == TERN_Q2_0_G128 ? 2 * (e & 1) : L == TERN_Q1_0_G128 ? (e & 3) : 0;
 }
 
-// int8 form of one unit u of one row of x, the tok-th of its column tile. xv: this lane's activations. scr: 32 x 8 words of this warp;
+// What the int8 form's rounding takes from fp16 activations, multiples of 2^-24 below 2^-12: in a list while it fits. The
+// list's order changes from run to run, so its sums are taken in integers.
+constexpr int kMaxLost = 256;
+struct Lost {
+  uint32_t marks[32];     // bit u mod 1024: an activation of unit u was rounded
+  int count;              // rounded activations, those past the list's end among them
+  int pad[3];
+  uint2 list[kMaxLost];   // k | row of x << 31, what is missing times 2^24
+};
+
+// int8 form of one unit u of row t of x, the tok-th of its column tile. xv: this lane's activations. scr: 32 x 8 words of this warp;
 // frag: the column tile's entries, then one 16-byte record for each q: accumulator starts of columns 2 q
 // and 2 q + 1 (binary: their sum to be added to twice the accumulators) and the scale 2^-S (x 2^16 for
-// digits 2 and 3). Non-finite activations count as zero here (the caller adds them apart) and set *odd. lost (EXACT): bit
-// u mod 1024 is set if an activation was rounded.
+// digits 2 and 3). Non-finite activations count as zero here (the caller adds them apart) and set *odd. lost (EXACT)
+// receives what rounding takes, its list only if `list`.
 template <int L, bool EXACT>
-__device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int tok, int u, uint32_t* scr, uint4* frag, int* odd, uint32_t* lost) {
+__device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int t, int tok, int u, uint32_t* scr, uint4* frag, int* odd, Lost* lost, bool list) {
   using T = Lay<L>;
   using G = Geo<L, kInt8>;
   const int lane = threadIdx.x & 31;
@@ -310,7 +322,20 @@ __device__ __forceinline__ void build_int8(float (&xv)[Lay<L>::kUnitK / 32], int
                      __float_as_uint(exp2i((pl ? 16 : 0) - Ss)), 0u);
     __syncwarp();
   }
-  if (coarse && __any_sync(0xffffffffu, rounded) && lane == 0) atomicOr(lost + (u >> 5 & 31), 1u << (u & 31));
+  if (coarse && __any_sync(0xffffffffu, rounded)) {
+    if (lane == 0) atomicOr(lost->marks + (u >> 5 & 31), 1u << (u & 31));
+#pragma unroll 1
+    for (int e = 0; list && e < NE; e++) {
+      float x = xv[0];
+#pragma unroll
+      for (int i = 1; i < NE; i++) x = e == i ? xv[i] : x;
+      const int Se = S[lane * NE + e < edge ? 0 : 1] - code_shift<L>(e);
+      const float v = x * exp2i(Se), d = v - rintf(v);
+      if (d == 0.f) continue;
+      const int i = atomicAdd(&lost->count, 1);
+      if (i < kMaxLost) lost->list[i] = make_uint2((uint32_t)(u * T::kUnitK + lane * NE + e) | (uint32_t)t << 31, (uint32_t)__float2int_rn(d * exp2i(24 - Se)));
+    }
+  }
 }
 
 // fp16 form of one (unit, column tile from row t0 of x on): lane (g, q) loads and writes the operand words of
@@ -434,7 +459,7 @@ struct Product {
   // 4-byte boundary below the first on
   static constexpr int kScaleBytes = L == TERN_Q2_0_G128 ? 8 : 16;
   static constexpr int kStage = 16 * 128 + 16 * kScaleBytes;  // [16][128] codes, [16][kScaleBytes] scales
-  static constexpr int kFlags = 64 + (MODE == kInt8 ? 128 : 0);  // bytes: `odd`, `lost`
+  static constexpr int kFlags = 64 + (MODE == kInt8 && L != TERN_Q1_0_G128 ? (int)sizeof(Lost) : 0);  // bytes: `odd`, `lost`
   static bool plan(int tiles, int units, size_t room, Split* out);
 
   // shared memory: operands [pass], partial sums [batch][wk][16][kRows], flags, scratch of the int8 operands'
@@ -600,6 +625,37 @@ struct Product {
     }
   }
 
+  // Adds the list's terms to the first partial sums of tiles [b0, b1), eight lanes for each output row. Scales and what is
+  // missing are multiples of 2^-24, below 2^16 and 2^-12, so 256 terms fit 64 bits. (A scale that is not finite has made
+  // the sum infinite or NaN already.)
+  static __device__ __forceinline__ void add_listed(const uint2* list, int n, float* part, int wk, const Mat& M, const Map& R, int b0,
+                                                    int b1, int tokens) {
+    const int sub = threadIdx.x & 7;
+    for (int i = threadIdx.x >> 3; i < (b1 - b0) * 16; i += kThreads / 8) {  // (a tile is four warps' rows: all lanes go on)
+      const int tl = i >> 4, r = i & 15;
+      const int64_t o = (int64_t)(b0 + tl) * R.step, last = min((int64_t)R.limit - 1 - o, (int64_t)64);
+      const int64_t row = r < 8 ? R.first + o + min((int64_t)r, last) : R.second + o + min((int64_t)(r - 8 + R.ahead), last);
+      const uint8_t* codes = M.codes + row * M.cstride;
+      const uint16_t* scales = M.scales + row * M.sstride;
+      int64_t z[kRows] = {};
+#pragma unroll 4
+      for (int j = sub; j < n; j += 8) {
+        const uint2 e = list[j];
+        const int k = (int)(e.x & 0x7fffffffu);
+        const float w = h2f(scales[k / kGroup]) * decode_t(L, codes, k);
+        const int64_t term = fabsf(w) <= 65504.f ? (int64_t)__float2ll_rn(w * 16777216.f) * (int)e.y : 0;
+#pragma unroll
+        for (int t = 0; t < kRows; t++) z[t] += (int)(e.x >> 31) == t ? term : 0;
+      }
+#pragma unroll
+      for (int t = 0; t < kRows; t++) {
+#pragma unroll
+        for (int d = 4; d; d >>= 1) z[t] += __shfl_xor_sync(0xffffffffu, z[t], d);
+        if (sub == 0 && t < tokens) part[(size_t)tl * wk * 16 * kRows + r * kRows + t] += (float)((double)z[t] * (1. / 281474976710656.));
+      }
+    }
+  }
+
   // Adds what the integers leave out of the activations in the units marked in `lost` to the first partial sums of tiles
   // [b0, b1): a warp takes four rows of a tile, a lane its byte of each unit. Units of an equal mark add zeros.
   template <class X>
@@ -672,7 +728,7 @@ struct Product {
     float* part = reinterpret_cast<float*>(smem + (size_t)s.pass * kBlk * kUnitBytes);
     uint8_t* tail = smem + (size_t)s.pass * kBlk * kUnitBytes + part_bytes(s);
     int* odd = reinterpret_cast<int*>(tail);  // rows of x with a non-finite activation
-    uint32_t* lost = reinterpret_cast<uint32_t*>(tail + 64);  // int8: bit u mod 1024: activations of unit u were rounded
+    Lost* lost = reinterpret_cast<Lost*>(tail + 64);  // int8, but for binary
     uint32_t* scr = reinterpret_cast<uint32_t*>(tail + kFlags) + warp * 256;
     const uint32_t ring = ((sm100::smem_u32(tail) + kFlags + (MODE == kInt8 ? kMaxWarps * 1024 : 0) + 127) & ~127u) + warp * (kDepth * kStage);
     const int blocks = (M.units + kBlk - 1) / kBlk;
@@ -708,7 +764,8 @@ struct Product {
     bool fresh = true;
     constexpr bool kLost = MODE == kInt8 && L != TERN_Q1_0_G128 && X::kExact;
     if (tid < 16) odd[tid] = 0;
-    if (kLost && tid < 32) lost[tid] = 0;
+    if (kLost && tid < 32) lost->marks[tid] = 0;
+    if (kLost && tid == 0) lost->count = 0;
     for (int b0 = t0; b0 < t1; b0 += s.batch) {
       const int b1 = min(t1, b0 + s.batch);
       int ta = b0, tb = b0;
@@ -767,8 +824,8 @@ struct Product {
               for (int e = 0; e < NE; e++) xv[e] = ahead[e];
               fetch(i + kMaxWarps);
               const int t = kRows == 1 || i < nu ? 0 : 1, u = i < nu ? i : i - nu;
-              build_int8<L, kLost>(xv, t % G::kTok, u0 + u, scr, reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes),
-                            odd + t, lost);
+              build_int8<L, kLost>(xv, t, t % G::kTok, u0 + u, scr, reinterpret_cast<uint4*>(frag + (size_t)u * kUnitBytes + (t / G::kTok) * G::kTileBytes),
+                            odd + t, lost, b0 == t0);
             }
           } else {
             uint32_t ahead[kLaneWords<L>] = {};
@@ -848,8 +905,9 @@ struct Product {
       }
       __syncthreads();
       if constexpr (kLost) {
-        if (__any_sync(0xffffffffu, lost[lane] != 0)) {
-          add_lost(lost, part, wk, M, R, b0, b1, xs, tokens);
+        if (lost->count) {
+          if (lost->count > kMaxLost) add_lost(lost->marks, part, wk, M, R, b0, b1, xs, tokens);
+          else add_listed(lost->list, lost->count, part, wk, M, R, b0, b1, tokens);
           __syncthreads();
         }
       }

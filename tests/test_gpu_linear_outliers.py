@@ -118,3 +118,57 @@ def test_experts_that_two_tokens_share(layout):
     assert np.array_equal(ids.cpu().numpy(), L.moe(*args)[2])
     assert np.bincount(ids.cpu().numpy().ravel()).max() > 1
     check(y.cpu().numpy(), L.moe(*args)[0], L.moe_bound(*args, held="integers"), "shared experts")
+
+
+def _few_tiny(seed, m, k, count):
+    """x with huge, ordinary and `count` tiny activations, the tiny ones alone below what stands beside the huge ones; their places."""
+    rng = np.random.default_rng(seed)
+    x = (np.round(rng.standard_normal((m, k)) * 64) / 64).astype(np.float16)
+    x[:, rng.choice(k, 5, replace=False)] = 30000.0
+    tiny = rng.choice(np.flatnonzero(x[0] < 100), count, replace=False)
+    x[:, tiny] = (rng.standard_normal((m, count)) * 1e-3).astype(np.float16)
+    return x, tiny
+
+
+@pytest.mark.parametrize("layout", [T.Q2_0_G128, T.T3_5PB_G128])
+@pytest.mark.parametrize("k,count", [(640, 1), (640, 30), (4224, 200), (4224, 1200), (38400, 250)])
+@pytest.mark.parametrize("gated", [False, True])
+def test_outputs_of_the_tiny_activations_alone(layout, k, count, gated):
+    # weights at every other activation are zero; few and many of the tiny ones stand beside a huge one
+    from tests.gpu_cases import pack_rows
+    n0, times = 64, 150
+    x, tiny = _few_tiny(15, 1, k, count)
+    t = np.zeros((n0, k), np.int8)
+    t[:, tiny] = np.random.default_rng(16).integers(-1, 2, (n0, count))
+    s = half(17, n0, k // 128, scale=0.05)
+    w = t * np.repeat(f64(s), 128, axis=1)
+    W = T.from_packed(_dev(np.tile(pack_rows(t, layout), (times, 1))), _dev(np.tile(s, (times, 1))), layout, k)
+    act = "relu" if gated else "none"
+    args = (np.concatenate([w, w]) if gated else w, f64(x), None, act, gated)
+    scale = 2.0 ** 10 if gated else 1.0  # a gate times an up sum of 1e-3 would fall below fp16's steps
+    if gated:
+        W.scales *= scale
+        args = (args[0] * scale,) + args[1:]
+    y = T.linear(W, _dev(x), act=act, gated=gated)
+    check(y[:, :n0].cpu().numpy(), L.linear(*args), L.linear_bound(*args, common=False), "tiny alone")
+    assert torch.equal(y, y[:, :n0].repeat(1, y.shape[1] // n0))
+    for _ in range(5):
+        assert torch.equal(y, T.linear(W, _dev(x), act=act, gated=gated))
+
+
+@pytest.mark.parametrize("layout", [T.Q2_0_G128, T.T3_5PB_G128])
+def test_tiny_activations_of_tokens_that_share_experts(layout):
+    from tests.gpu_cases import pack_rows
+    experts, d, f, tokens, top_k = 24, 640, 384, 3, 4
+    x, tiny = _few_tiny(18, tokens, d, 30)
+    t = np.zeros((experts * 2 * f, d), np.int8)
+    t[:, tiny] = np.random.default_rng(19).integers(-1, 2, (t.shape[0], 30))
+    gs = half(20, experts * 2 * f, d // 128, scale=16.0)
+    gw = t * np.repeat(f64(gs), 128, axis=1)
+    dc, ds, dw = weights(layout, experts * d, f, 21, scale=1.0)
+    G, D = T.from_packed(_dev(pack_rows(t, layout)), _dev(gs), layout, d), T.from_packed(_dev(dc), _dev(ds), layout, f)
+    r = half(22, experts, d, scale=1e-3)
+    args = (gw.reshape(experts, 2 * f, d), dw.reshape(experts, d, f), f64(r), f64(x), top_k, "relu", True)
+    y, _, ids = T.moe(G, D, _dev(r), _dev(x), top_k, act="relu", return_routing=True)
+    assert np.array_equal(ids.cpu().numpy(), L.moe(*args)[2])
+    check(y.cpu().numpy(), L.moe(*args)[0], L.moe_bound(*args, held="integers"), "shared experts")
